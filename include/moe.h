@@ -587,6 +587,194 @@ moe_status_t moe_unpermute_combine_bwd(const void* d_out, const void* y, int dty
                                        const int32_t* row_map, const float* topk_w, int T,
                                        int k, int d, void* d_y, float* d_topk_w, void* stream);
 
+/* ---------------------------------------------------------------- block norms
+ * Root-mean-square norms before and after a block, fused with the block's gate,
+ * the residual scale and, optionally, the combine that closes the MoE layer
+ * (moe_unpermute_combine).  With N(v) = v / sqrt(mean_c v_c^2 + eps):
+ *   y[t]  = y[t], or sum_j topk_w[t,j] y[row_map[t,j]]  (row_map given)
+ *   n     = N(y) * w_post                 (w_post NULL: n = y)
+ *   h1[t] = res_scale * h[t] + row_gate[t] * gate * n   (each gate NULL: 1)
+ *   x     = N(h1) * w_pre                 (w_pre NULL: no x)
+ * y NULL: h1 = h, only x is computed (the norm in front of the first block).
+ * Everything between the loads and the stores is float32: h1 and the combined
+ * y enter the norms unrounded, each output is rounded once.
+ *   h [T, d] dtype, the residual stream;
+ *   y [T, d] dtype, the block's output, or [T*k, d] expert rows with row_map
+ *     [T, k] and topk_w [T, k] float32 (nullable: unit weights), as
+ *     moe_unpermute_combine takes them (ids outside [0, T*k) read row 0);
+ *   w_post, gate, w_pre [d] float32, row_gate [T] float32, each nullable;
+ *   h_out [T, d] dtype = h1 (with y; may be h or y itself);
+ *   x_out [T, d] dtype = x (with w_pre; may be h or y itself);
+ *   y_out [T, d] dtype (nullable, only with row_map): the combined y, which
+ *     the backward reads.
+ * With row_map no output may share memory with y; outputs never overlap each
+ * other, nor an input except as the very same tensor.  dtype MOE_F32 or
+ * MOE_BF16; d * element size a multiple of 16, at most 65536 bytes
+ * (MOE_ERR_UNSUPPORTED above); eps > 0. */
+typedef struct {
+  size_t struct_size; /* = sizeof(moe_block_norm_fwd_args_t) */
+  int dtype;
+  int T, d, k;        /* k: with row_map */
+  float res_scale, eps;
+  const void* h;
+  const void* y;
+  const float* w_post;
+  const float* gate;
+  const float* row_gate;
+  const float* w_pre;
+  const int32_t* row_map;
+  const float* topk_w;
+  void* h_out;
+  void* x_out;
+  void* y_out;
+} moe_block_norm_fwd_args_t;
+moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* args, void* stream);
+
+/* Gradients of the above, given dh1 (the gradient of h1 from whatever else
+ * reads it, nullable: 0) and dx (the gradient of x; given iff w_pre is):
+ *   D = dh1 + dN(h1)^T (dx * w_pre)                  the whole gradient of h1
+ *   dh = res_scale * D                               (y NULL: dh = D)
+ *   dy = dN(y)^T (row_gate * gate * w_post * D)      the combined y's gradient
+ *   dw_pre = sum_t dx N(h1), dw_post = sum_t D row_gate gate N(y),
+ *   dgate = sum_t D row_gate w_post N(y), drow_gate[t] = sum_c D gate w_post N(y)
+ * (without w_post: n = y in place of N(y) w_post).  h1 [T, d] (read only with dx)
+ * and y [T, d] are the forward's stored tensors (h_out; y or y_out); the norms'
+ * statistics are taken from them again.  dy is moe_unpermute_combine_bwd's d_out.
+ *   dh [T, d], dy [T, d] dtype (out; each may be one of the inputs h1, y, dh1,
+ *   dx itself); dw_pre, dw_post, dgate [d] and drow_gate [T] float32 (out,
+ *   nullable).  `accumulate` adds the three channel gradients (not drow_gate)
+ *   to the existing values.  ws: moe_block_norm_bwd_workspace_size(T, d) bytes,
+ *   needed with dw_pre, dw_post or dgate (else MOE_ERR_WORKSPACE). */
+typedef struct {
+  size_t struct_size; /* = sizeof(moe_block_norm_bwd_args_t) */
+  int dtype;
+  int T, d;
+  float res_scale, eps;
+  int accumulate;
+  const void* h1;
+  const void* y;
+  const void* dh1;
+  const void* dx;
+  const float* w_post;
+  const float* gate;
+  const float* row_gate;
+  const float* w_pre;
+  void* dh;
+  void* dy;
+  float* dw_post;
+  float* dgate;
+  float* drow_gate;
+  float* dw_pre;
+  void* ws;
+  size_t ws_bytes;
+} moe_block_norm_bwd_args_t;
+size_t moe_block_norm_bwd_workspace_size(int T, int d);
+moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* args, void* stream);
+
+/* ---------------------------------------------------------------- gradient norm
+ * The norm of many tensors taken together, and clipping by it:
+ *   norm = sqrt(sum over the tensors and their elements of g^2)
+ *   c    = min(1, max_norm / (norm + eps)),  out_i = c * data_i
+ * Squares are summed in float64 in a fixed order, the norm is rounded to float32
+ * once; c is computed in float64 and rounded to float32 once; data * c is a
+ * float32 product, rounded once to out's type.  A norm of
+ * infinity gives c = 0, a NaN norm gives NaN everywhere.
+ *   tensors [n]: a HOST array, read during the call only; data and out are
+ *     device pointers aligned to their element size; numel may be 0; dtype and
+ *     out_dtype are MOE_F32 or MOE_BF16.  moe_grad_norm reads data, numel and
+ *     dtype only.
+ *   out == data (of one type) clips in place; otherwise no out may share memory
+ *     with any data, any other out, norm or ws (MOE_ERR_INVALID_ARG: a tensor
+ *     listed twice cannot be clipped in place).
+ *   norm: float32 device word (out).
+ *   ws: moe_grad_norm_workspace_size(n) bytes, 16-byte aligned; its contents
+ *     need no clearing, but calls that may overlap need one each.
+ * max_norm >= 0 (infinity: never clips), eps > 0. */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t numel;
+  int dtype;
+  int out_dtype;
+} moe_tensor_t;
+size_t moe_grad_norm_workspace_size(int n);
+moe_status_t moe_grad_norm(const moe_tensor_t* tensors, int n, float* norm, void* ws,
+                           size_t ws_bytes, void* stream);
+moe_status_t moe_clip_grad_norm(const moe_tensor_t* tensors, int n, double max_norm, double eps,
+                                float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- adapters
+ * Low-rank adapters of many requests beside a shared projection y = x W^T
+ * (moe_grouped_gemm_fwd with E = 1).  The rows of a batch are grouped by
+ * adapter as expert segments are: position p in [offsets[a], offsets[a+1])
+ * belongs to adapter a < NA and stands for row src_row[p] of x and y (src_row
+ * NULL: row p).  Positions from offsets[NA] on have no adapter.
+ * moe_permute with k = 1 and E = NA + 1, the id NA meaning "none", gives
+ * offsets and src_row for a batch's adapter ids; one such plan serves every
+ * projection the batch passes.
+ *   v[p]   = x[t] A[a]^T                      (float32)
+ *   out[t] = y[t] + scale[a] * v[p] B[a]^T    (float32, rounded once)
+ * Rows without an adapter are copied (untouched when out == y).
+ *   dtype MOE_BF16 (MOE_F32: MOE_ERR_UNSUPPORTED); x [T, K], y, out [T, N];
+ *   A [NA, r, K], B [NA, N, r]; scale [NA] float32 (nullable: 1);
+ *   v_out [T, r] float32 (nullable): v by position, for the backward; rows
+ *     without an adapter are not written.
+ *   src_row, if given, a permutation of [0, T); entries outside [0, T) are
+ *     skipped.  out may be y; it overlaps nothing else.
+ *   ws: moe_lora_workspace_size(T, K, N, r, NA) bytes (both directions).
+ * K and N multiples of 32, r a multiple of 8 up to 128 (more:
+ * MOE_ERR_UNSUPPORTED), 1 <= NA < MOE_MAX_EXPERTS. */
+typedef struct {
+  size_t struct_size; /* = sizeof(moe_lora_fwd_args_t) */
+  int dtype;
+  int T, K, N, r, NA;
+  const void* x;
+  const void* A;
+  const void* B;
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* src_row;
+  const void* y;
+  void* out;
+  float* v_out;
+  void* ws;
+  size_t ws_bytes;
+} moe_lora_fwd_args_t;
+size_t moe_lora_workspace_size(int T, int K, int N, int r, int NA);
+moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* args, void* stream);
+
+/* Backward, given dy [T, N] bf16 and the forward's v [T, r] float32:
+ *   u[p]      = scale[a] * dy[t] B[a]              (float32)
+ *   dx_out[t] = dx[t] + u[p] A[a]                  (bf16, rounded once; dx NULL: 0)
+ *   dA[a]     = sum_p u[p]^T x[t]                  [NA, r, K] float32
+ *   dB[a]     = scale[a] * sum_p dy[t]^T v[p]      [NA, N, r] float32
+ * dx is the shared projection's gradient (moe_grouped_gemm_bwd, DGRAD); rows
+ * without an adapter keep it.  Any of dx_out (may be dx), dA and dB may be
+ * NULL, not all; dA and dB of an adapter without rows are exact zeros, or left
+ * as they were with `accumulate`, which adds to the existing values.  Sums run
+ * in a fixed order (no atomics). */
+typedef struct {
+  size_t struct_size; /* = sizeof(moe_lora_bwd_args_t) */
+  int dtype;
+  int T, K, N, r, NA;
+  int accumulate;
+  const void* x;       /* for dA */
+  const void* dy;
+  const void* A;       /* for dx_out */
+  const void* B;       /* for dx_out and dA */
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* src_row;
+  const float* v;      /* for dB */
+  const void* dx;
+  void* dx_out;
+  float* dA;
+  float* dB;
+  void* ws;
+  size_t ws_bytes;
+} moe_lora_bwd_args_t;
+moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

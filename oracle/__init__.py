@@ -8,5 +8,7 @@ generator ``synth`` is the only module both sides use.
 ``oracle.moe``: routing, permutation, FC1 weight repack, GLU activations,
 grouped GEMMs, combine and the whole forward / backward chain in float64.
 ``oracle.mx``: the OCP MXFP8 codec (E4M3 elements, E8M0 block scales).
+``oracle.block``: block norms with gate and residual scale, gradient-norm
+clipping, low-rank adapters.
 """
-from . import moe, mx  # noqa: F401
+from . import block, moe, mx  # noqa: F401

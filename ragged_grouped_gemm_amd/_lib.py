@@ -68,6 +68,47 @@ class GemmBwdArgs(ctypes.Structure):
                 ("a_src_rows", c_int), ("out_mx", _PMX), ("wt", c_void_p)]
 
 
+class BlockNormFwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", c_size_t), ("dtype", c_int), ("T", c_int), ("d", c_int),
+                ("k", c_int), ("res_scale", c_float), ("eps", c_float), ("h", c_void_p),
+                ("y", c_void_p), ("w_post", c_void_p), ("gate", c_void_p), ("row_gate", c_void_p),
+                ("w_pre", c_void_p), ("row_map", c_void_p), ("topk_w", c_void_p),
+                ("h_out", c_void_p), ("x_out", c_void_p), ("y_out", c_void_p)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", c_size_t), ("dtype", c_int), ("T", c_int), ("d", c_int),
+                ("res_scale", c_float), ("eps", c_float), ("accumulate", c_int), ("h1", c_void_p),
+                ("y", c_void_p), ("dh1", c_void_p), ("dx", c_void_p), ("w_post", c_void_p),
+                ("gate", c_void_p), ("row_gate", c_void_p), ("w_pre", c_void_p), ("dh", c_void_p),
+                ("dy", c_void_p), ("dw_post", c_void_p), ("dgate", c_void_p),
+                ("drow_gate", c_void_p), ("dw_pre", c_void_p), ("ws", c_void_p),
+                ("ws_bytes", c_size_t)]
+
+
+class TensorT(ctypes.Structure):
+    """moe_tensor_t: one tensor of a gradient list."""
+    _fields_ = [("data", c_void_p), ("out", c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", c_int), ("out_dtype", c_int)]
+
+
+class LoraFwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", c_size_t), ("dtype", c_int), ("T", c_int), ("K", c_int),
+                ("N", c_int), ("r", c_int), ("NA", c_int), ("x", c_void_p), ("A", c_void_p),
+                ("B", c_void_p), ("scale", c_void_p), ("offsets", c_void_p), ("src_row", c_void_p),
+                ("y", c_void_p), ("out", c_void_p), ("v_out", c_void_p), ("ws", c_void_p),
+                ("ws_bytes", c_size_t)]
+
+
+class LoraBwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", c_size_t), ("dtype", c_int), ("T", c_int), ("K", c_int),
+                ("N", c_int), ("r", c_int), ("NA", c_int), ("accumulate", c_int), ("x", c_void_p),
+                ("dy", c_void_p), ("A", c_void_p), ("B", c_void_p), ("scale", c_void_p),
+                ("offsets", c_void_p), ("src_row", c_void_p), ("v", c_void_p), ("dx", c_void_p),
+                ("dx_out", c_void_p), ("dA", c_void_p), ("dB", c_void_p), ("ws", c_void_p),
+                ("ws_bytes", c_size_t)]
+
+
 _SIGS = {
     "moe_version": (ctypes.c_char_p, []),
     "moe_status_string": (ctypes.c_char_p, [c_int]),
@@ -115,6 +156,17 @@ _SIGS = {
     "moe_mxfp4_quantize_experts": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int,
                                            c_void_p, c_void_p, c_int, c_int, c_int, _PMX, _PMX,
                                            c_void_p]),
+    "moe_block_norm_fwd": (c_int, [ctypes.POINTER(BlockNormFwdArgs), c_void_p]),
+    "moe_block_norm_bwd_workspace_size": (c_size_t, [c_int, c_int]),
+    "moe_block_norm_bwd": (c_int, [ctypes.POINTER(BlockNormBwdArgs), c_void_p]),
+    "moe_grad_norm_workspace_size": (c_size_t, [c_int]),
+    "moe_grad_norm": (c_int, [ctypes.POINTER(TensorT), c_int, c_void_p, c_void_p, c_size_t,
+                              c_void_p]),
+    "moe_clip_grad_norm": (c_int, [ctypes.POINTER(TensorT), c_int, ctypes.c_double,
+                                   ctypes.c_double, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_lora_workspace_size": (c_size_t, [c_int] * 5),
+    "moe_lora_fwd": (c_int, [ctypes.POINTER(LoraFwdArgs), c_void_p]),
+    "moe_lora_bwd": (c_int, [ctypes.POINTER(LoraBwdArgs), c_void_p]),
 }
 
 _lib = None

@@ -8,7 +8,7 @@ passed in (preallocated, e.g. for graph capture) or are allocated here.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -528,3 +528,259 @@ def moe_unpermute_combine_bwd(d_out, y, row_map, topk_w, d_y=None, d_topk_w=None
                                                 _stream()),
           "moe_unpermute_combine_bwd")
     return d_y, d_topk_w
+
+
+# ------------------------------------------------------------------ block norms, clipping, adapters
+
+
+def _ptr(t, shape, dtype, dev, name, optional=False):
+    """Address of an argument of the given shape and type on dev (None if optional)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
+
+
+def _workspace(ws, nbytes, dev):
+    """(address, bytes) of the caller's workspace, or of a new one (returned to be kept)."""
+    if ws is None:
+        ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and live on {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def moe_block_norm_fwd(h, y=None, *, w_post=None, gate=None, row_gate=None, res_scale=1.0,
+                       w_pre=None, eps=1e-6, row_map=None, topk_w=None, h_out=None, x_out=None,
+                       y_out=None, want_y=False):
+    """The residual h [T, d] joined by a block's output y, and the next block's
+    normed input, in one pass (N(v) = v / sqrt(mean(v^2) + eps)):
+
+        h1 = res_scale h + row_gate gate N(y) w_post,   x = N(h1) w_pre
+
+    w_post None: y joins as it is; w_pre None: no x; y None: only x = N(h) w_pre.
+    gate [d] and row_gate [T] are optional float32 factors per channel and per
+    token.  With row_map [T, k] (and topk_w), y holds the expert rows [T*k, d]
+    and is combined first (moe_unpermute_combine); y_out, or want_y, keeps the
+    combined y for the backward.  Returns (h1 or None, x or None, y_out or None).
+    """
+    if h.dim() != 2:
+        raise ValueError("h must be [T, d]")
+    T, d = h.shape
+    dt, dev, f32 = h.dtype, h.device, torch.float32
+    k = 0
+    if row_map is not None:
+        k = row_map.shape[-1]
+        if want_y and y_out is None:
+            y_out = torch.empty_like(h)
+    elif want_y:
+        raise ValueError("want_y goes with row_map (y is the combined output already)")
+    if y is not None and h_out is None:
+        h_out = torch.empty_like(h)
+    if w_pre is not None and x_out is None:
+        x_out = torch.empty_like(h)
+    args = _lib.BlockNormFwdArgs(
+        ctypes.sizeof(_lib.BlockNormFwdArgs), _dtype(h), T, d, k, res_scale, eps,
+        _ptr(h, (T, d), dt, dev, "h"), _ptr(y, (T * max(k, 1), d), dt, dev, "y", True),
+        _ptr(w_post, (d,), f32, dev, "w_post", True), _ptr(gate, (d,), f32, dev, "gate", True),
+        _ptr(row_gate, (T,), f32, dev, "row_gate", True), _ptr(w_pre, (d,), f32, dev, "w_pre", True),
+        _ptr(row_map, (T, k), torch.int32, dev, "row_map", True),
+        _ptr(topk_w, (T, k), f32, dev, "topk_w", True), _ptr(h_out, (T, d), dt, dev, "h_out", True),
+        _ptr(x_out, (T, d), dt, dev, "x_out", True), _ptr(y_out, (T, d), dt, dev, "y_out", True))
+    check(_call(dev, _lib.load().moe_block_norm_fwd, ctypes.byref(args)), "moe_block_norm_fwd")
+    return h_out, x_out, y_out
+
+
+class BlockNormGrads(NamedTuple):
+    """moe_block_norm_bwd's results; None where an input was not given."""
+    dh: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    drow_gate: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+
+
+def moe_block_norm_bwd_workspace_size(T, d) -> int:
+    return int(_lib.load().moe_block_norm_bwd_workspace_size(T, d))
+
+
+def moe_block_norm_bwd(h1, y=None, *, dh1=None, dx=None, w_post=None, gate=None, row_gate=None,
+                       res_scale=1.0, w_pre=None, eps=1e-6, dh=None, dy=None, dw_post=None,
+                       dgate=None, drow_gate=None, dw_pre=None, accumulate=False,
+                       ws=None) -> BlockNormGrads:
+    """Gradients of moe_block_norm_fwd from its stored h1 and y (the combined y
+    where the forward combined), the gradient dh1 of h1 and dx of x (each may
+    be None: zero; dx comes with w_pre).  accumulate adds dw_post, dgate and
+    dw_pre to the given tensors."""
+    ref = h1 if h1 is not None else y
+    if ref is None or ref.dim() != 2:
+        raise ValueError("h1 (or y) must be [T, d]")
+    T, d = ref.shape
+    dt, dev, f32 = ref.dtype, ref.device, torch.float32
+    if accumulate and any(w is not None and g is None for w, g in
+                          ((w_post, dw_post), (gate, dgate), (w_pre, dw_pre))):
+        raise ValueError("accumulate needs the gradients to add to")
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    dh = new((T, d), dt) if dh is None else dh
+    if y is not None and dy is None:
+        dy = new((T, d), dt)
+    if w_post is not None and dw_post is None:
+        dw_post = new((d,), f32)
+    if gate is not None and dgate is None:
+        dgate = new((d,), f32)
+    if row_gate is not None and drow_gate is None:
+        drow_gate = new((T,), f32)
+    if w_pre is not None and dw_pre is None:
+        dw_pre = new((d,), f32)
+    ws, wp, wb = _workspace(ws, moe_block_norm_bwd_workspace_size(T, d), dev)
+    args = _lib.BlockNormBwdArgs(
+        ctypes.sizeof(_lib.BlockNormBwdArgs), _dtype(ref), T, d, res_scale, eps, int(accumulate),
+        _ptr(h1, (T, d), dt, dev, "h1", True), _ptr(y, (T, d), dt, dev, "y", True),
+        _ptr(dh1, (T, d), dt, dev, "dh1", True), _ptr(dx, (T, d), dt, dev, "dx", True),
+        _ptr(w_post, (d,), f32, dev, "w_post", True), _ptr(gate, (d,), f32, dev, "gate", True),
+        _ptr(row_gate, (T,), f32, dev, "row_gate", True), _ptr(w_pre, (d,), f32, dev, "w_pre", True),
+        _ptr(dh, (T, d), dt, dev, "dh"), _ptr(dy, (T, d), dt, dev, "dy", True),
+        _ptr(dw_post, (d,), f32, dev, "dw_post", True), _ptr(dgate, (d,), f32, dev, "dgate", True),
+        _ptr(drow_gate, (T,), f32, dev, "drow_gate", True),
+        _ptr(dw_pre, (d,), f32, dev, "dw_pre", True), wp, wb)
+    check(_call(dev, _lib.load().moe_block_norm_bwd, ctypes.byref(args)), "moe_block_norm_bwd")
+    return BlockNormGrads(dh, dy, dw_post, dgate, drow_gate, dw_pre)
+
+
+def _tensor_list(grads, out):
+    """The ctypes moe_tensor_t array of the tensors (out: None, or one tensor per gradient)."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError("an empty list of tensors")
+    if out is not None and len(out) != n:
+        raise ValueError(f"{len(out)} outputs for {n} tensors")
+    dev = grads[0].device
+    arr = (_lib.TensorT * n)()
+    for i, g in enumerate(grads):
+        o = g if out is None else out[i]
+        if o.shape != g.shape:
+            raise ValueError(f"out[{i}] must be {tuple(g.shape)}, got {tuple(o.shape)}")
+        if g.device != dev or o.device != dev:
+            raise ValueError("all tensors must live on one GPU")
+        if not (g.is_contiguous() and o.is_contiguous()):
+            raise ValueError("tensors must be contiguous")
+        arr[i] = (g.data_ptr(), o.data_ptr(), g.numel(), _dtype(g), _dtype(o))
+    return arr, n, dev
+
+
+def moe_grad_norm_workspace_size(n) -> int:
+    return int(_lib.load().moe_grad_norm_workspace_size(n))
+
+
+def moe_grad_norm(grads, *, norm=None, ws=None):
+    """sqrt of the sum of squares of all elements of the tensors (float32 or
+    bfloat16, summed in float64), as a float32 tensor [1] on their device."""
+    arr, n, dev = _tensor_list(grads, None)
+    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
+    ws, wp, wb = _workspace(ws, moe_grad_norm_workspace_size(n), dev)
+    check(_call(dev, _lib.load().moe_grad_norm, arr, n, _ptr(norm, (1,), torch.float32, dev, "norm"),
+                wp, wb), "moe_grad_norm")
+    return norm
+
+
+def moe_clip_grad_norm(grads, max_norm, *, out=None, eps=1e-6, norm=None, ws=None):
+    """Scale the tensors by min(1, max_norm / (norm + eps)), norm their global
+    norm (moe_grad_norm), in place or into ``out`` (one tensor per gradient, of
+    either type).  Returns the norm before clipping, float32 [1]; nothing is
+    read back to the host."""
+    arr, n, dev = _tensor_list(grads, out)
+    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
+    ws, wp, wb = _workspace(ws, moe_grad_norm_workspace_size(n), dev)
+    check(_call(dev, _lib.load().moe_clip_grad_norm, arr, n, max_norm, eps,
+                _ptr(norm, (1,), torch.float32, dev, "norm"), wp, wb), "moe_clip_grad_norm")
+    return norm
+
+
+def moe_lora_workspace_size(T, K, N, r, NA) -> int:
+    return int(_lib.load().moe_lora_workspace_size(T, K, N, r, NA))
+
+
+def _lora_sizes(x, A, B, offsets):
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [T, K], A [NA, r, K] and B [NA, N, r]")
+    T, K = x.shape
+    NA, r, _ = A.shape
+    if offsets.dim() != 1 or offsets.shape[0] <= NA:
+        raise ValueError("offsets must hold NA + 1 entries or more")
+    return T, K, B.shape[1], r, NA
+
+
+def moe_lora_fwd(x, A, B, offsets, y, *, src_row=None, scale=None, out=None, v_out=None,
+                 want_v=False, ws=None):
+    """out[t] = y[t] + scale[a] (x[t] A[a]^T) B[a]^T for the adapter a of each row
+    (bf16; A [NA, r, K], B [NA, N, r]).  Position p in [offsets[a], offsets[a+1])
+    is row src_row[p] (src_row None: row p); rows past offsets[NA] have no
+    adapter.  ``moe_permute(None, ids.view(T, 1), NA + 1, gather=False)``, with
+    the id NA for "none", gives offsets and src_row.  out None: y in place.
+    Returns (out, v or None); v = x A^T [T, r] float32, by position, with v_out
+    or want_v (for moe_lora_bwd)."""
+    T, K, N, r, NA = _lora_sizes(x, A, B, offsets)
+    bf, f32, dev = x.dtype, torch.float32, x.device
+    out = y if out is None else out
+    if want_v and v_out is None:
+        v_out = torch.zeros((T, r), dtype=f32, device=dev)
+    ws, wp, wb = _workspace(ws, moe_lora_workspace_size(T, K, N, r, NA), dev)
+    args = _lib.LoraFwdArgs(
+        ctypes.sizeof(_lib.LoraFwdArgs), _dtype(x), T, K, N, r, NA, _ptr(x, (T, K), bf, dev, "x"),
+        _ptr(A, (NA, r, K), bf, dev, "A"), _ptr(B, (NA, N, r), bf, dev, "B"),
+        _ptr(scale, (NA,), f32, dev, "scale", True),
+        _ptr(offsets, offsets.shape, torch.int32, dev, "offsets"),
+        _ptr(src_row, (T,), torch.int32, dev, "src_row", True), _ptr(y, (T, N), bf, dev, "y"),
+        _ptr(out, (T, N), bf, dev, "out"), _ptr(v_out, (T, r), f32, dev, "v_out", True), wp, wb)
+    check(_call(dev, _lib.load().moe_lora_fwd, ctypes.byref(args)), "moe_lora_fwd")
+    return out, v_out
+
+
+def moe_lora_bwd(x, dy, A, B, offsets, v, *, src_row=None, scale=None, dx=None, dx_out=None,
+                 want_dx=True, dA=None, dB=None, want_dw=True, accumulate=False, ws=None):
+    """Gradients of moe_lora_fwd: with u = scale[a] dy B[a],
+    dx_out = dx + u A[a] (dx the shared projection's input gradient, or None;
+    dx_out None: dx in place, or a new tensor), dA[a] = u^T x and
+    dB[a] = scale[a] dy^T v, float32, v the forward's.  Returns (dx_out, dA, dB)."""
+    T, K, N, r, NA = _lora_sizes(x, A, B, offsets)
+    bf, f32, dev = x.dtype, torch.float32, x.device
+    if accumulate and want_dw and (dA is None or dB is None):
+        raise ValueError("accumulate needs the gradients to add to")
+    if want_dx and dx_out is None:
+        dx_out = torch.empty_like(x) if dx is None else dx
+    if want_dw:
+        dA = torch.empty(A.shape, dtype=f32, device=dev) if dA is None else dA
+        dB = torch.empty(B.shape, dtype=f32, device=dev) if dB is None else dB
+    ws, wp, wb = _workspace(ws, moe_lora_workspace_size(T, K, N, r, NA), dev)
+    args = _lib.LoraBwdArgs(
+        ctypes.sizeof(_lib.LoraBwdArgs), _dtype(x), T, K, N, r, NA, int(accumulate),
+        _ptr(x, (T, K), bf, dev, "x"), _ptr(dy, (T, N), bf, dev, "dy"),
+        _ptr(A, (NA, r, K), bf, dev, "A"), _ptr(B, (NA, N, r), bf, dev, "B"),
+        _ptr(scale, (NA,), f32, dev, "scale", True),
+        _ptr(offsets, offsets.shape, torch.int32, dev, "offsets"),
+        _ptr(src_row, (T,), torch.int32, dev, "src_row", True),
+        _ptr(v, (T, r), f32, dev, "v", True), _ptr(dx, (T, K), bf, dev, "dx", True),
+        _ptr(dx_out, (T, K), bf, dev, "dx_out", True), _ptr(dA, (NA, r, K), f32, dev, "dA", True),
+        _ptr(dB, (NA, N, r), f32, dev, "dB", True), wp, wb)
+    check(_call(dev, _lib.load().moe_lora_bwd, ctypes.byref(args)), "moe_lora_bwd")
+    return dx_out, dA, dB
