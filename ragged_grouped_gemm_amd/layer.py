@@ -69,6 +69,10 @@ expert-segmented column copies written straight from x and d_out; FC1's
 epilogue writes A, and the dGLU epilogue dH, as the same two copies; H stays
 bf16 for the dGLU.  Weights are quantized once (``mx_weights``) into row and
 transposed copies.
+
+``MoEBlock`` puts the layer into a residual stream: the norm before it, the
+combine fused with the norm after it, its gate, the residual and the next
+block's norm, their gradients, and clipping by the global gradient norm.
 """
 from __future__ import annotations
 
@@ -257,6 +261,14 @@ class MoEFFN:
                                    dx=self.dX)
 
     def forward(self, x, logits, W1p, W2, b1p=None, b2=None):
+        self.forward_rows(x, logits, W1p, W2, b1p, b2)
+        with self._op("combine"):
+            ops.moe_unpermute_combine(self.Y, self.row_map, self.combine_weights(), out=self.out)
+        return self.out
+
+    def forward_rows(self, x, logits, W1p, W2, b1p=None, b2=None):
+        """The forward up to the expert rows Y [R, d], before the combine
+        (out[t] = sum_j combine_weights()[t, j] Y[row_map[t, j]])."""
         if self.mx:
             return self._forward_mx(x, logits, W1p)
         self._route(x, logits)
@@ -273,16 +285,14 @@ class MoEFFN:
         with self._op("fc2_fwd"):
             ops.moe_grouped_gemm_fwd(self.A, W2, self.offsets, b=b2, y=self.Y,
                                      max_cus=self.max_cus)
-        with self._op("combine"):
-            ops.moe_unpermute_combine(self.Y, self.row_map, self._combine_w(), out=self.out)
-        return self.out
+        return self.Y
 
     def _gates_to_rows(self):
         if self.gate_in_act:
             with self._op("gates_to_rows"):
                 ops.moe_permute_rows(self.topk_w, self.row_map, out=self.w_row)
 
-    def _combine_w(self):
+    def combine_weights(self):
         """Gates of the combine: unit weights when they scale FC1's activation."""
         return None if self.gate_in_act else self.topk_w
 
@@ -375,9 +385,7 @@ class MoEFFN:
         with self._op("fc2_fwd"):
             ops.moe_grouped_gemm_fwd(self.A_row, W.w2, self.offsets, E=E, N=d, y=self.Y,
                                      max_cus=self.max_cus)
-        with self._op("combine"):
-            ops.moe_unpermute_combine(self.Y, self.row_map, self._combine_w(), out=self.out)
-        return self.out
+        return self.Y
 
     def _backward_mx(self, d_out, logits, W: MXWeights):
         E, R, d = self.E, self.R, self.d
@@ -390,7 +398,7 @@ class MoEFFN:
             ops.moe_mx_quantize_experts(d_out, self.offsets, self.pad_offsets, R,
                                         src_row=self.src_row,
                                         row_map=None if self.gate_in_act else self.row_map,
-                                        topk_w=self._combine_w(), row_out=self.dY_row,
+                                        topk_w=self.combine_weights(), row_out=self.dY_row,
                                         col_out=self.dY_col)
         with self._op("fc2_dgrad_dglu"):
             ops.moe_grouped_gemm_glu_bwd(self.dY_row, W.w2t, self.H, self.offsets, E=E,
@@ -445,6 +453,106 @@ class MoEFFN:
         with torch.cuda.graph(g):
             self.step(x, logits, W1p, W2, d_out, b1p, b2)
         return g
+
+
+class MoEBlock:
+    """The layer with its surroundings in a residual stream h [T, d]:
+
+        x  = N(h) w_pre                      (x given: the previous block made it)
+        h1 = res_scale h + gate N(MoE(x)) w_post
+        x' = N(h1) next_w_pre                (the next block's input, optional)
+
+    with N(v) = v / sqrt(mean(v^2) + eps); w_post and gate [d] float32 are
+    optional.  The combine of the expert rows, the norm after the layer, gate,
+    residual and the next block's norm are one launch (moe_block_norm_fwd), and
+    one more goes back through them (moe_block_norm_bwd).  ``ffn`` is a MoEFFN
+    of any variant; the block adds buffers from the same ``alloc``.
+
+    Stacked blocks pass (h1, x') on and (dh, dX) back:
+        h, x = a.forward(h, x, ..., next_w_pre=w_b)
+        h, x = b.forward(h, x, ...)
+        dh, dX = b.backward(dh, None, ...);  dh, dX = a.backward(dh, dX, ...)
+    A block that computed its own x (x=None) returns dh complete and dX = None.
+    """
+
+    def __init__(self, ffn: MoEFFN, *, res_scale=1.0, eps=1e-6, alloc=None):
+        self.ffn, self.res_scale, self.eps = ffn, res_scale, eps
+        T, d, dev = ffn.T, ffn.d, ffn.topk_w.device
+
+        def z(shape, dt):
+            return (torch.zeros(shape, dtype=dt, device=dev) if alloc is None else
+                    alloc(tuple(shape), dt, dev))
+
+        dt, f32 = ffn.dtype, torch.float32
+        self.x_own, self.h1, self.x_next = z((T, d), dt), z((T, d), dt), z((T, d), dt)
+        self.saved = None
+        if ffn.has_backward:
+            self.dh_res, self.dh, self.dy = (z((T, d), dt) for _ in range(3))
+            self.dw_pre, self.dw_post, self.dgate, self.dw_next = (z((d,), f32) for _ in range(4))
+            self.ws = z((ops.moe_block_norm_bwd_workspace_size(T, d),), torch.uint8)
+            self.norm = z((1,), f32)
+            self.clip_ws = z((ops.moe_grad_norm_workspace_size(0),), torch.uint8)
+            self.grads = []
+        self.y = ffn.out                 # the combined output, which the backward reads
+
+    def forward(self, h, x, logits, W1p, W2, b1p=None, b2=None, *, w_pre=None, w_post=None,
+                gate=None, next_w_pre=None):
+        """Returns (h1, x' or None).  logits, W1p, W2, b1p, b2 as MoEFFN.forward.
+        h, and x or the weights, must not change before the backward."""
+        L = self.ffn
+        if (x is None) == (w_pre is None):
+            raise ValueError("give the block either its normed input x or its norm's weight w_pre")
+        if x is None:
+            with L._op("norm_pre"):
+                x = ops.moe_block_norm_fwd(h, w_pre=w_pre, eps=self.eps, x_out=self.x_own)[1]
+        Y = L.forward_rows(x, logits, W1p, W2, b1p, b2)
+        with L._op("combine_norm"):
+            _, xn, _ = ops.moe_block_norm_fwd(
+                h, Y, w_post=w_post, gate=gate, res_scale=self.res_scale, w_pre=next_w_pre,
+                eps=self.eps, row_map=L.row_map, topk_w=L.combine_weights(), h_out=self.h1,
+                x_out=self.x_next if next_w_pre is not None else None,
+                y_out=self.y if L.has_backward else None)
+        self.saved = (h, w_pre, w_post, gate, next_w_pre)
+        return self.h1, xn
+
+    def backward(self, dh1, dx_next, logits, W1p, W2):
+        """The gradients of h1 and of x' (None where nothing reads x').  Returns
+        (dh, None), or (dh, dX) when x was given; weight gradients are in the
+        layer (dW1p, dW2, ...) and in dw_pre, dw_post, dgate, dw_next."""
+        L = self.ffn
+        if not L.has_backward:
+            raise RuntimeError("layer built without backward buffers")
+        if self.saved is None:
+            raise RuntimeError("backward before forward")
+        h, w_pre, w_post, gate, next_w_pre = self.saved
+        used = dx_next is not None
+        if used and next_w_pre is None:
+            raise ValueError("the forward made no input for a next block")
+        with L._op("norm_post_bwd"):
+            g = ops.moe_block_norm_bwd(
+                self.h1 if used else None, self.y, dh1=dh1, dx=dx_next, w_post=w_post, gate=gate,
+                res_scale=self.res_scale, w_pre=next_w_pre if used else None, eps=self.eps,
+                dh=self.dh_res, dy=self.dy, dw_post=self.dw_post if w_post is not None else None,
+                dgate=self.dgate if gate is not None else None,
+                dw_pre=self.dw_next if used else None, ws=self.ws)
+        self.grads = [t for t in (g.dw_post, g.dgate, g.dw_pre) if t is not None]
+        dX = L.backward(g.dy, logits, W1p, W2)
+        self.grads += [t for t in (L.dW1p, L.dW2, L.db1p, L.db2, L.dWr) if t is not None]
+        if w_pre is None:
+            return self.dh_res, dX
+        with L._op("norm_pre_bwd"):
+            ops.moe_block_norm_bwd(h, dh1=self.dh_res, dx=dX, w_pre=w_pre, eps=self.eps, dh=self.dh,
+                                   dw_pre=self.dw_pre, ws=self.ws)
+        self.grads.append(self.dw_pre)
+        return self.dh, None
+
+    def clip_grads(self, max_norm, more=()):
+        """Scale the block's weight gradients (and the tensors in ``more``, e.g. of
+        adapters or other blocks: their ``grads``) in place by
+        min(1, max_norm / (norm + 1e-6)); returns their norm before, on the device."""
+        with self.ffn._op("clip"):
+            return ops.moe_clip_grad_norm([*self.grads, *more], max_norm, norm=self.norm,
+                                          ws=self.clip_ws)
 
 
 class OpTimer:
