@@ -28,6 +28,9 @@
 #include <math.h>
 #include <stddef.h>
 
+#include <algorithm>
+#include <type_traits>
+
 namespace moe {
 
 // TPR threads share a row; a thread owns chunks tid, tid + TPR, ... (NC of them).
@@ -64,6 +67,18 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* lds, int half) {
   }
 }
 
+// pack_chunk with the hardware's conversion (round to nearest even, two values
+// an instruction): the bit arithmetic of f32_to_bf16_bits costs about seven,
+// which these kernels, at 25 to 40 operations per element, would feel.
+__device__ __forceinline__ u32x4 store_chunk(const float* v, BF16) {
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  f32x8 f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = v[i];
+  return __builtin_bit_cast(u32x4, __builtin_convertvector(f, bf16x8));
+}
+__device__ __forceinline__ u32x4 store_chunk(const float* v, F32) { return pack_chunk(v, F32()); }
+
 // V consecutive floats of a per-channel vector (NULL: `fill`).
 template <int V>
 __device__ __forceinline__ void load_chan(const float* p, size_t c, float* v, float fill) {
@@ -90,45 +105,101 @@ struct NormFwd {
   float res_scale, eps, inv_d;
 };
 
-template <class EL, int TPR, int NC>
+// y[t]'s chunk c from its expert rows, four rows' loads in flight.
+template <class EL>
+__device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, float* y) {
+  constexpr int V = EL::VEC;
+  const int32_t* ids = p.row_map + (size_t)t * p.k;
+  const float* ws = p.topk_w ? p.topk_w + (size_t)t * p.k : nullptr;
+#pragma unroll
+  for (int q = 0; q < V; ++q) y[q] = 0.0f;
+  auto add = [&](auto N, int j0) {
+    constexpr int n = decltype(N)::value;
+    u32x4 raw[n];
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      int r = ids[j0 + j];
+      r = (r < 0 || r >= p.R) ? 0 : r;
+      raw[j] = p.y[(size_t)r * p.chunks + c];
+    }
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float w = ws ? ws[j0 + j] : 1.0f;
+      float v[V];
+      unpack_chunk(raw[j], v, EL());
+#pragma unroll
+      for (int q = 0; q < V; ++q) y[q] = fmaf(w, v[q], y[q]);
+    }
+  };
+  int j = 0;
+  for (; j + 4 <= p.k; j += 4) add(std::integral_constant<int, 4>(), j);
+  for (; j < p.k; ++j) add(std::integral_constant<int, 1>(), j);
+}
+
+// Blocks walk the rows; a row's loads are issued while the one before it is
+// reduced, and the channel vectors stay in registers throughout.
+template <class EL, int TPR, int NC, bool POST, bool PRE, bool COMB>
 __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(const NormFwd p) {
   typedef NormGeom<TPR> G;
   constexpr int V = EL::VEC;
+  constexpr bool LOADY = POST && !COMB;
   __shared__ float lds[2 * G::WPR * 4];
   const int lt = threadIdx.x % TPR;
-  for (int t = blockIdx.x * G::RPB + threadIdx.x / TPR; t < p.T; t += gridDim.x * G::RPB) {
-    const size_t row = (size_t)t * p.chunks;
-    float h[NC][V];
+  // (uniform over a wave)
+  int t = __builtin_amdgcn_readfirstlane(blockIdx.x * G::RPB + threadIdx.x / TPR);
+  const int step = gridDim.x * G::RPB;
+  bool in[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) in[i] = lt + i * TPR < p.chunks;
+  u32x4 hr[NC], yr[NC];
+  const u32x4 zero = {0, 0, 0, 0};
+  auto fetch = [&](int row) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = lt + i * TPR;
-#pragma unroll
-      for (int q = 0; q < V; ++q) h[i][q] = 0.0f;
-      if (c < p.chunks) unpack_chunk(p.h[row + c], h[i], EL());
+      const size_t o = (size_t)row * p.chunks + lt + i * TPR;
+      hr[i] = in[i] && row < p.T ? p.h[o] : zero;
+      if constexpr (LOADY) yr[i] = in[i] && row < p.T ? p.y[o] : zero;
     }
-    if (p.y) {
-      float y[NC][V];
+  };
+  fetch(t);
+  float wg[NC][V], wp[NC][V];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) wg[i][q] = wp[i][q] = 0.0f;
+    if (in[i]) {
+      const int c = lt + i * TPR;
+      if constexpr (POST) {
+        float g[V];
+        load_chan<V>(p.w_post, c, wg[i], 1.0f);
+        load_chan<V>(p.gate, c, g, 1.0f);
+#pragma unroll
+        for (int q = 0; q < V; ++q) wg[i][q] *= g[q];
+      }
+      if constexpr (PRE) load_chan<V>(p.w_pre, c, wp[i], 1.0f);
+    }
+  }
+  for (; t < p.T; t += step) {
+    const size_t row = (size_t)t * p.chunks + lt;
+    float h[NC][V], y[NC][V];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      unpack_chunk(hr[i], h[i], EL());
+      if constexpr (LOADY) unpack_chunk(yr[i], y[i], EL());
+    }
+    fetch(t + step);
+    if constexpr (POST) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-#pragma unroll
-        for (int q = 0; q < V; ++q) y[i][q] = 0.0f;
-        if (c < p.chunks) {
-          if (p.row_map) {
-            for (int j = 0; j < p.k; ++j) {
-              int r = p.row_map[(size_t)t * p.k + j];
-              r = (r < 0 || r >= p.R) ? 0 : r;
-              const float w = p.topk_w ? p.topk_w[(size_t)t * p.k + j] : 1.0f;
-              float v[V];
-              unpack_chunk(p.y[(size_t)r * p.chunks + c], v, EL());
-#pragma unroll
-              for (int q = 0; q < V; ++q) y[i][q] = fmaf(w, v[q], y[i][q]);
-            }
+        if constexpr (COMB) {
+          if (in[i]) {
+            combine_chunk<EL>(p, t, lt + i * TPR, y[i]);
+            if (p.y_out) p.y_out[row + i * TPR] = store_chunk(y[i], EL());
           } else {
-            unpack_chunk(p.y[row + c], y[i], EL());
+#pragma unroll
+            for (int q = 0; q < V; ++q) y[i][q] = 0.0f;
           }
-          if (p.y_out) p.y_out[row + c] = pack_chunk(y[i], EL());
         }
 #pragma unroll
         for (int q = 0; q < V; ++q) s[0] = fmaf(y[i][q], y[i][q], s[0]);
@@ -140,19 +211,12 @@ __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        if (c < p.chunks) {
-          float w[V], g[V];
-          load_chan<V>(p.w_post, c, w, 1.0f);
-          load_chan<V>(p.gate, c, g, 1.0f);
 #pragma unroll
-          for (int q = 0; q < V; ++q)
-            h[i][q] = fmaf(p.res_scale, h[i][q], y[i][q] * f * (w[q] * g[q]));
-          p.h_out[row + c] = pack_chunk(h[i], EL());
-        }
+        for (int q = 0; q < V; ++q) h[i][q] = fmaf(p.res_scale, h[i][q], y[i][q] * (f * wg[i][q]));
+        if (in[i]) p.h_out[row + i * TPR] = store_chunk(h[i], EL());
       }
     }
-    if (p.x_out) {
+    if constexpr (PRE) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NC; ++i)
@@ -162,19 +226,14 @@ __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(
       const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        if (c < p.chunks) {
-          float w[V];
-          load_chan<V>(p.w_pre, c, w, 1.0f);
 #pragma unroll
-          for (int q = 0; q < V; ++q) h[i][q] = h[i][q] * r * w[q];
-          p.x_out[row + c] = pack_chunk(h[i], EL());
-        }
+        for (int q = 0; q < V; ++q) h[i][q] *= r * wp[i][q];
+        if (in[i]) p.x_out[row + i * TPR] = store_chunk(h[i], EL());
       }
     }
     // a row with only one of the two reductions meets the same LDS half again
     // in the next step
-    if (TPR > 64 && !(p.w_post && p.y && p.x_out)) __syncthreads();
+    if (TPR > 64 && !(PRE && POST && p.w_post)) __syncthreads();
   }
 }
 
@@ -371,13 +430,21 @@ template <class EL>
 struct LaunchNormFwd {
   const NormFwd& p;
   hipStream_t s;
-  template <int TPR, int NC>
-  moe_status_t run() const {
+  template <int TPR, int NC, bool POST, bool PRE, bool COMB>
+  moe_status_t go() const {
     typedef NormGeom<TPR> G;
     const int groups = (p.T + G::RPB - 1) / G::RPB;
-    hipLaunchKernelGGL((block_norm_fwd_kernel<EL, TPR, NC>), dim3(groups), dim3(G::THREADS), 0, s,
-                       p);
+    const int blocks = std::min(groups, device_cu_count() * (2048 / G::THREADS) / 2);
+    hipLaunchKernelGGL((block_norm_fwd_kernel<EL, TPR, NC, POST, PRE, COMB>), dim3(blocks),
+                       dim3(G::THREADS), 0, s, p);
     return launch_status();
+  }
+  template <int TPR, int NC>
+  moe_status_t run() const {
+    if (!p.y) return go<TPR, NC, false, true, false>();
+    if (p.row_map)
+      return p.x_out ? go<TPR, NC, true, true, true>() : go<TPR, NC, true, false, true>();
+    return p.x_out ? go<TPR, NC, true, true, false>() : go<TPR, NC, true, false, false>();
   }
 };
 

@@ -7,6 +7,7 @@ passed in (preallocated, e.g. for graph capture) or are allocated here.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 from typing import NamedTuple, Optional
 
@@ -554,10 +555,11 @@ def _call(dev, fn, *args):
     """fn(*args, stream) on dev's current stream, with dev the current device."""
     if dev.type != "cuda":
         raise ValueError("tensors must live on the GPU")
+    # the raw handle costs 0.1 us, torch.cuda.current_stream() 2.8 us of a 12 us call
     if dev.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def _workspace(ws, nbytes, dev):
@@ -675,17 +677,27 @@ def _tensor_list(grads, out):
     if out is not None and len(out) != n:
         raise ValueError(f"{len(out)} outputs for {n} tensors")
     dev = grads[0].device
-    arr = (_lib.TensorT * n)()
-    for i, g in enumerate(grads):
-        o = g if out is None else out[i]
-        if o.shape != g.shape:
-            raise ValueError(f"out[{i}] must be {tuple(g.shape)}, got {tuple(o.shape)}")
-        if g.device != dev or o.device != dev:
-            raise ValueError("all tensors must live on one GPU")
-        if not (g.is_contiguous() and o.is_contiguous()):
-            raise ValueError("tensors must be contiguous")
-        arr[i] = (g.data_ptr(), o.data_ptr(), g.numel(), _dtype(g), _dtype(o))
-    return arr, n, dev
+    # attribute by attribute: a list of each costs less than a loop body per tensor
+    tensors = grads if out is None else [*grads, *out]
+    if len(set(map(torch.Tensor.get_device, tensors))) != 1:
+        raise ValueError("all tensors must live on one GPU")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError("tensors must be contiguous")
+    if out is not None and [t.shape for t in grads] != [t.shape for t in out]:
+        raise ValueError("out must have the shapes of the tensors")
+    ptrs = list(map(torch.Tensor.data_ptr, tensors))
+    kinds = [t.dtype for t in tensors]
+    bad = set(kinds) - _DT.keys()
+    if bad:
+        raise TypeError(f"unsupported dtype {bad.pop()} (float32 or bfloat16)")
+    kinds = [_DT[k] for k in kinds]
+    # moe_tensor_t is four 8-byte words: data, out, numel, dtype | out_dtype << 32
+    words = array.array("q", bytes(32 * n))
+    words[0::4] = array.array("q", ptrs[:n])
+    words[1::4] = array.array("q", ptrs[-n:])
+    words[2::4] = array.array("q", list(map(torch.Tensor.numel, grads)))
+    words[3::4] = array.array("q", [a | b << 32 for a, b in zip(kinds, kinds[-n:])])
+    return (_lib.TensorT * n).from_buffer(words), n, dev
 
 
 def moe_grad_norm_workspace_size(n) -> int:
