@@ -33,37 +33,46 @@
 
 namespace moe {
 
-// TPR threads share a row; a thread owns chunks tid, tid + TPR, ... (NC of them).
-template <int TPR>
-struct NormGeom {
-  static constexpr int THREADS = TPR < 256 ? 256 : TPR;
-  static constexpr int RPB = THREADS / TPR;      // rows per block and step
-  static constexpr int WPR = TPR / 64;           // waves per row
+// A row belongs to one wave (WROW: rows of up to 64 NC chunks, several to a
+// block) or to a whole block of ceil(chunks / (64 NC)) waves.  A lane owns the
+// 16-byte chunks lt, lt + tpr, ... of its row (NC of them; tpr lanes a row), so
+// only the last wave of a row can have idle lanes.
+template <bool WROW>
+struct NormPlace {
+  int tpr, lt, sub;      // lanes per row; lane within the row; row within the block
+  __device__ __forceinline__ NormPlace()
+      : tpr(WROW ? 64 : blockDim.x),
+        lt(WROW ? threadIdx.x & 63 : threadIdx.x),
+        sub(WROW ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0) {}
 };
 
-// Sums of NV values over the TPR threads of a row, on every thread.  A wave's
-// butterfly, then the row's waves in order through LDS.  `buf` alternates
+// Sums of NV <= 4 values over a row's lanes, on every lane.  A wave's
+// butterfly, then one over the row's waves through LDS.  `half` alternates
 // between two halves: a thread writes one half again only after the barrier
 // of the other, which every thread reaches after reading the first.
-template <int NV, int TPR>
-__device__ __forceinline__ void row_sums(float (&v)[NV], float* lds, int half) {
+template <int NV, bool WROW>
+__device__ __forceinline__ void row_sums(float (&v)[NV], f32x4 (*lds)[16], int half) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (TPR > 64) {
-    constexpr int WPR = TPR / 64;
-    float* b = lds + half * (WPR * 4);
-    const int w = threadIdx.x >> 6;
+  if constexpr (!WROW) {
+    f32x4* b = lds[half];
     if ((threadIdx.x & 63) == 0) {
+      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) b[w * 4 + i] = v[i];
+      for (int i = 0; i < NV; ++i) o[i] = v[i];
+      b[threadIdx.x >> 6] = o;
     }
     __syncthreads();
+    // each group of 16 lanes adds the waves' sums in a butterfly
+    const int w = threadIdx.x & 15;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (w < (int)(blockDim.x >> 6)) o = b[w];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = 0.0f;
+    for (int i = 0; i < NV; ++i) {
+      v[i] = o[i];
 #pragma unroll
-    for (int j = 0; j < WPR; ++j)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] += b[j * 4 + i];
+      for (int m = 8; m >= 1; m >>= 1) v[i] += __shfl_xor(v[i], m, 16);
+    }
   }
 }
 
@@ -138,16 +147,15 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
 
 // Blocks walk the rows; a row's loads are issued while the one before it is
 // reduced, and the channel vectors stay in registers throughout.
-template <class EL, int TPR, int NC, bool POST, bool PRE, bool COMB>
-__global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(const NormFwd p) {
-  typedef NormGeom<TPR> G;
+template <class EL, int NC, bool WROW, bool POST, bool PRE, bool COMB>
+__global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
   constexpr int V = EL::VEC;
   constexpr bool LOADY = POST && !COMB;
-  __shared__ float lds[2 * G::WPR * 4];
-  const int lt = threadIdx.x % TPR;
-  // (uniform over a wave)
-  int t = __builtin_amdgcn_readfirstlane(blockIdx.x * G::RPB + threadIdx.x / TPR);
-  const int step = gridDim.x * G::RPB;
+  __shared__ f32x4 lds[2][16];
+  const NormPlace<WROW> pl;
+  const int lt = pl.lt, TPR = pl.tpr, rpb = WROW ? blockDim.x >> 6 : 1;
+  int t = blockIdx.x * rpb + pl.sub;
+  const int step = gridDim.x * rpb;
   bool in[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) in[i] = lt + i * TPR < p.chunks;
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(
       }
       float f = p.row_gate ? p.row_gate[t] : 1.0f;
       if (p.w_post) {
-        row_sums<1, TPR>(s, lds, 0);
+        row_sums<1, WROW>(s, lds, 0);
         f *= 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
       }
 #pragma unroll
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int q = 0; q < V; ++q) s[0] = fmaf(h[i][q], h[i][q], s[0]);
-      row_sums<1, TPR>(s, lds, 1);
+      row_sums<1, WROW>(s, lds, 1);
       const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_fwd_kernel(
     }
     // a row with only one of the two reductions meets the same LDS half again
     // in the next step
-    if (TPR > 64 && !(PRE && POST && p.w_post)) __syncthreads();
+    if (!WROW && !(PRE && POST && p.w_post)) __syncthreads();
   }
 }
 
@@ -242,138 +250,163 @@ struct NormBwd {
   const float *w_post, *gate, *row_gate, *w_pre;
   u32x4 *dh, *dy;
   float* drow_gate;
-  float *part_pre, *part_post;   // [gridDim.x * RPB][d] sums of the rows a row group walked
+  float *part_pre, *part_post;   // [gridDim.x][d] sums of the rows a block walked
   int T, chunks;
   float res_scale, eps, inv_d;
 };
 
-template <class EL, int TPR, int NC>
-__global__ void __launch_bounds__(NormGeom<TPR>::THREADS) block_norm_bwd_kernel(const NormBwd p) {
-  typedef NormGeom<TPR> G;
+template <class EL, int NC, bool WROW, bool POST, bool PRE>
+__global__ void __launch_bounds__(WROW && NC > 1 ? 512 : 1024) block_norm_bwd_kernel(
+    const NormBwd p) {
   constexpr int V = EL::VEC;
-  __shared__ float lds[2 * G::WPR * 4];
-  const int lt = threadIdx.x % TPR;
-  float apre[NC][V], apost[NC][V];
+  __shared__ f32x4 lds[2][16];
+  const NormPlace<WROW> pl;
+  const int lt = pl.lt, TPR = pl.tpr, rpb = WROW ? blockDim.x >> 6 : 1;
+  const int step = gridDim.x * rpb;
+  bool in[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
+  for (int i = 0; i < NC; ++i) in[i] = lt + i * TPR < p.chunks;
+  u32x4 hr[NC], zr[NC], yr[NC], gr[NC];
+  const u32x4 zero = {0, 0, 0, 0};
+  auto fetch = [&](int row) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) apre[i][q] = apost[i][q] = 0.0f;
-  for (int t = blockIdx.x * G::RPB + threadIdx.x / TPR; t < p.T; t += gridDim.x * G::RPB) {
-    const size_t row = (size_t)t * p.chunks;
+    for (int i = 0; i < NC; ++i) {
+      const size_t o = (size_t)row * p.chunks + lt + i * TPR;
+      const bool ok = in[i] && row < p.T;
+      gr[i] = ok && p.dh1 ? p.dh1[o] : zero;
+      if constexpr (PRE) {
+        hr[i] = ok ? p.h1[o] : zero;
+        zr[i] = ok ? p.dx[o] : zero;
+      }
+      if constexpr (POST) yr[i] = ok ? p.y[o] : zero;
+    }
+  };
+  int t = blockIdx.x * rpb + pl.sub;
+  fetch(t);
+  float wg[NC][V], wp[NC][V], apre[NC][V], apost[NC][V];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) wg[i][q] = wp[i][q] = apre[i][q] = apost[i][q] = 0.0f;
+    if (in[i]) {
+      const int c = lt + i * TPR;
+      if constexpr (POST) {
+        float g[V];
+        load_chan<V>(p.w_post, c, wg[i], 1.0f);
+        load_chan<V>(p.gate, c, g, 1.0f);
+#pragma unroll
+        for (int q = 0; q < V; ++q) wg[i][q] *= g[q];
+      }
+      if constexpr (PRE) load_chan<V>(p.w_pre, c, wp[i], 1.0f);
+    }
+  }
+  for (; t < p.T; t += step) {
+    const size_t row = (size_t)t * p.chunks + lt;
     float D[NC][V], h[NC][V], z[NC][V], y[NC][V];
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = lt + i * TPR;
-#pragma unroll
-      for (int q = 0; q < V; ++q) D[i][q] = h[i][q] = z[i][q] = y[i][q] = 0.0f;
-      if (c < p.chunks) {
-        if (p.dh1) unpack_chunk(p.dh1[row + c], D[i], EL());
-        if (p.dx) {
-          unpack_chunk(p.h1[row + c], h[i], EL());
-          unpack_chunk(p.dx[row + c], z[i], EL());
-        }
-        if (p.y) unpack_chunk(p.y[row + c], y[i], EL());
+      unpack_chunk(gr[i], D[i], EL());
+      if constexpr (PRE) {
+        unpack_chunk(hr[i], h[i], EL());
+        unpack_chunk(zr[i], z[i], EL());
       }
+      if constexpr (POST) unpack_chunk(yr[i], y[i], EL());
     }
-    if (p.dx) {
+    fetch(t + step);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        float w[V];
-        if (c < p.chunks) load_chan<V>(p.w_pre, c, w, 1.0f);
+    for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
+      for (int q = 0; q < V; ++q) {
+        if constexpr (PRE) {
           s[0] = fmaf(h[i][q], h[i][q], s[0]);
-          if (c < p.chunks) s[1] = fmaf(z[i][q] * w[q], h[i][q], s[1]);
+          s[1] = fmaf(z[i][q] * wp[i][q], h[i][q], s[1]);
         }
+        if constexpr (POST) s[2] = fmaf(y[i][q], y[i][q], s[2]);
       }
-    }
-    if (p.y && p.w_post) {
+    if (PRE || p.w_post) row_sums<3, WROW>(s, lds, 0);
+    if constexpr (PRE) {
+      const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
+      const float m = -r * r * (s[1] * p.inv_d);
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int q = 0; q < V; ++q) s[2] = fmaf(y[i][q], y[i][q], s[2]);
-    }
-    if (p.dx || (p.y && p.w_post)) row_sums<3, TPR>(s, lds, 0);
-    if (p.dx) {
-      const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
-      const float m = r * r * (s[1] * p.inv_d);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        if (c < p.chunks) {
-          float w[V];
-          load_chan<V>(p.w_pre, c, w, 1.0f);
-#pragma unroll
-          for (int q = 0; q < V; ++q) {
-            apre[i][q] = fmaf(z[i][q], h[i][q] * r, apre[i][q]);
-            D[i][q] = fmaf(r, fmaf(-h[i][q], m, z[i][q] * w[q]), D[i][q]);
-          }
+        for (int q = 0; q < V; ++q) {
+          const float zw = z[i][q] * wp[i][q];
+          apre[i][q] = fmaf(z[i][q], h[i][q] * r, apre[i][q]);
+          D[i][q] = fmaf(r, fmaf(h[i][q], m, zw), D[i][q]);
         }
-      }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = lt + i * TPR;
-      if (c < p.chunks) {
-        float o[V];
+      float o[V];
 #pragma unroll
-        for (int q = 0; q < V; ++q) o[q] = p.res_scale * D[i][q];
-        p.dh[row + c] = pack_chunk(o, EL());
-      }
+      for (int q = 0; q < V; ++q) o[q] = p.res_scale * D[i][q];
+      if (in[i]) p.dh[row + i * TPR] = store_chunk(o, EL());
     }
-    if (p.y) {
+    if constexpr (POST) {
       const float ry = p.w_post ? 1.0f / sqrtf(s[2] * p.inv_d + p.eps) : 1.0f;
-      const float rg = p.row_gate ? p.row_gate[t] : 1.0f;
+      const float f = ry * (p.row_gate ? p.row_gate[t] : 1.0f);
       float s2[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        if (c < p.chunks) {
-          float w[V], g[V];
-          load_chan<V>(p.w_post, c, w, 1.0f);
-          load_chan<V>(p.gate, c, g, 1.0f);
+      for (int i = 0; i < NC; ++i)
 #pragma unroll
-          for (int q = 0; q < V; ++q) {
-            apost[i][q] = fmaf(D[i][q], y[i][q] * (ry * rg), apost[i][q]);
-            D[i][q] *= w[q] * g[q];
-            s2[0] = fmaf(D[i][q], y[i][q], s2[0]);
-          }
+        for (int q = 0; q < V; ++q) {
+          apost[i][q] = fmaf(D[i][q], y[i][q] * f, apost[i][q]);
+          D[i][q] *= wg[i][q];
+          s2[0] = fmaf(D[i][q], y[i][q], s2[0]);
         }
-      }
-      if (p.w_post || p.drow_gate) row_sums<1, TPR>(s2, lds, 1);
+      if (p.w_post || p.drow_gate) row_sums<1, WROW>(s2, lds, 1);
       if (p.drow_gate && lt == 0) p.drow_gate[t] = ry * s2[0];
-      const float m = p.w_post ? ry * ry * (s2[0] * p.inv_d) : 0.0f;
+      const float m = p.w_post ? -f * (ry * ry * (s2[0] * p.inv_d)) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = lt + i * TPR;
-        if (c < p.chunks) {
-          float o[V];
+        float o[V];
 #pragma unroll
-          for (int q = 0; q < V; ++q) o[q] = ry * rg * fmaf(-y[i][q], m, D[i][q]);
-          p.dy[row + c] = pack_chunk(o, EL());
-        }
+        for (int q = 0; q < V; ++q) o[q] = fmaf(y[i][q], m, f * D[i][q]);
+        if (in[i]) p.dy[row + i * TPR] = store_chunk(o, EL());
       }
     }
-    if (TPR > 64) __syncthreads();
+    // a row with only one of the two reductions meets the same LDS half again
+    if (!WROW && !(POST && p.w_post)) __syncthreads();
   }
-  const size_t prow = ((size_t)blockIdx.x * G::RPB + threadIdx.x / TPR) * p.chunks * V;
+  // one row of sums per block: the rows of a block (one a wave) are added in order
+  auto put = [&](float* part, float (&a)[NC][V]) {
+    if (!part) return;
+    float* o = part + (size_t)blockIdx.x * p.chunks * V;
+    if constexpr (WROW) {
+      __shared__ float acc[NC * 64 * V];
+      for (int w = 0; w < rpb; ++w) {
+        __syncthreads();
+        if (w != pl.sub) continue;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = lt + i * TPR;
-    if (c < p.chunks) {
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int q = 0; q < V; q += 4) {
-        if (p.part_pre) store4(p.part_pre + prow + (size_t)c * V + q, &apre[i][q]);
-        if (p.part_post) store4(p.part_post + prow + (size_t)c * V + q, &apost[i][q]);
+          for (int q = 0; q < V; q += 4) {
+            float* s = acc + (lt + i * 64) * V + q;
+            f32x4 v = {a[i][q], a[i][q + 1], a[i][q + 2], a[i][q + 3]};
+            if (w) v = *reinterpret_cast<f32x4*>(s) + v;
+            *reinterpret_cast<f32x4*>(s) = v;
+          }
       }
+      __syncthreads();
+      for (int i = threadIdx.x; i < p.chunks * V / 4; i += blockDim.x)
+        reinterpret_cast<f32x4*>(o)[i] = reinterpret_cast<f32x4*>(acc)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int q = 0; q < V; q += 4)
+          if (in[i]) store4(o + (size_t)(lt + i * TPR) * V + q, &a[i][q]);
     }
-  }
+  };
+  if constexpr (PRE) put(p.part_pre, apre);
+  if constexpr (POST) put(p.part_post, apost);
 }
 
-// The channel gradients from the blocks' partial rows, added in order:
-// 16 waves share 64 columns, each summing every 16th row.
+// The channel gradients from the blocks' rows of sums, added in order: 32 groups
+// of lanes share 32 columns (128 bytes), each adding every 32nd row, eight loads
+// in flight.
 struct NormFinish {
   const float *part_pre, *part_post, *w_post, *gate;
   float *dw_pre, *dw_post, *dgate;
@@ -381,20 +414,29 @@ struct NormFinish {
 };
 
 __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const NormFinish p) {
-  __shared__ float lds[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float lds[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   const float* part = blockIdx.y ? p.part_post : p.part_pre;
   if (!part) return;
   float s = 0.0f;
-  if (c < p.d)
-    for (int r = w; r < p.rows; r += 16) s += part[(size_t)r * p.d + c];
+  if (c < p.d) {
+    int r = w;
+    for (; r + 7 * 32 < p.rows; r += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[(size_t)(r + 32 * i) * p.d + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; r < p.rows; r += 32) s += part[(size_t)r * p.d + c];
+  }
   lds[w][lane] = s;
   __syncthreads();
   if (w || c >= p.d) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s += lds[i][lane];
+  for (int i = 0; i < 32; ++i) s += lds[i][lane];
   auto put = [&](float* o, float v) {
     if (o) o[c] = p.accumulate ? o[c] + v : v;
   };
@@ -406,45 +448,60 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const NormFinis
   }
 }
 
-// Row groups of the backward's grid: a fixed number (not the card's CU count,
-// so that the order of the channel sums is the same everywhere).
-static constexpr int NORM_BWD_GROUPS = 512;
+// The geometry of a row: chunks per lane, and waves per row (0: a wave a row).
+struct NormGeom {
+  int nc, waves;
+};
+static NormGeom norm_geom(int chunks) {
+  if (chunks <= 64) return {1, 0};
+  if (chunks <= 128) return {2, 0};
+  const int nc = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  return {nc, (chunks + 64 * nc - 1) / (64 * nc)};
+}
 
-static int norm_groups(int T) { return T < NORM_BWD_GROUPS ? T : NORM_BWD_GROUPS; }
-
-// Calls f.template run<TPR, NC>() for a row of `chunks` 16-byte chunks.
+// Calls f.template run<NC, WROW>(waves per row) for a row of `chunks` chunks.
 template <class F>
 static moe_status_t norm_dispatch(int chunks, F&& f) {
-  if (chunks <= 64) return f.template run<64, 1>();
-  if (chunks <= 128) return f.template run<64, 2>();
-  if (chunks <= 256) return f.template run<256, 1>();
-  if (chunks <= 512) return f.template run<256, 2>();
-  if (chunks <= 1024) return f.template run<512, 2>();
-  if (chunks <= 2048) return f.template run<1024, 2>();
-  return f.template run<1024, 4>();
+  const NormGeom g = norm_geom(chunks);
+  if (!g.waves) return g.nc == 1 ? f.template run<1, true>(0) : f.template run<2, true>(0);
+  return g.nc == 1   ? f.template run<1, false>(g.waves)
+         : g.nc == 2 ? f.template run<2, false>(g.waves)
+                     : f.template run<4, false>(g.waves);
 }
 
 static constexpr int NORM_MAX_CHUNKS = 4096;
+// a row past the last one is still a positive int
+static constexpr int NORM_MAX_ROWS = INT32_MAX - (1 << 20);
+
+// Blocks of the backward: enough to fill 256 compute units with 8 to 16 waves
+// each, a fixed number (not the card's own count), so that the order of the
+// channel sums is the same everywhere.
+static int norm_bwd_blocks(int T, int chunks) {
+  const NormGeom g = norm_geom(chunks);
+  const int rpb = g.waves ? 1 : g.nc == 1 ? 16 : 8;
+  const int per_cu = g.waves ? std::max(1, std::min(4, 16 / g.waves)) : 1;
+  return std::min((T + rpb - 1) / rpb, 256 * per_cu);
+}
 
 template <class EL>
 struct LaunchNormFwd {
   const NormFwd& p;
   hipStream_t s;
-  template <int TPR, int NC, bool POST, bool PRE, bool COMB>
-  moe_status_t go() const {
-    typedef NormGeom<TPR> G;
-    const int groups = (p.T + G::RPB - 1) / G::RPB;
-    const int blocks = std::min(groups, device_cu_count() * (2048 / G::THREADS) / 2);
-    hipLaunchKernelGGL((block_norm_fwd_kernel<EL, TPR, NC, POST, PRE, COMB>), dim3(blocks),
-                       dim3(G::THREADS), 0, s, p);
+  template <int NC, bool WROW, bool POST, bool PRE, bool COMB>
+  moe_status_t go(int waves) const {
+    const int threads = WROW ? 256 : 64 * waves, rpb = WROW ? 4 : 1;
+    const int blocks = std::min((p.T + rpb - 1) / rpb,
+                                device_cu_count() * std::max(1, 1024 / threads));
+    hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB>), dim3(blocks),
+                       dim3(threads), 0, s, p);
     return launch_status();
   }
-  template <int TPR, int NC>
-  moe_status_t run() const {
-    if (!p.y) return go<TPR, NC, false, true, false>();
+  template <int NC, bool WROW>
+  moe_status_t run(int waves) const {
+    if (!p.y) return go<NC, WROW, false, true, false>(waves);
     if (p.row_map)
-      return p.x_out ? go<TPR, NC, true, true, true>() : go<TPR, NC, true, false, true>();
-    return p.x_out ? go<TPR, NC, true, true, false>() : go<TPR, NC, true, false, false>();
+      return p.x_out ? go<NC, WROW, true, true, true>(waves) : go<NC, WROW, true, false, true>(waves);
+    return p.x_out ? go<NC, WROW, true, true, false>(waves) : go<NC, WROW, true, false, false>(waves);
   }
 };
 
@@ -452,15 +509,18 @@ template <class EL>
 struct LaunchNormBwd {
   const NormBwd& p;
   hipStream_t s;
-  int* rows;      // partial rows written
-  template <int TPR, int NC>
-  moe_status_t run() const {
-    typedef NormGeom<TPR> G;
-    const int blocks = (norm_groups(p.T) + G::RPB - 1) / G::RPB;
-    *rows = blocks * G::RPB;
-    hipLaunchKernelGGL((block_norm_bwd_kernel<EL, TPR, NC>), dim3(blocks), dim3(G::THREADS), 0, s,
-                       p);
+  int blocks;
+  template <int NC, bool WROW, bool POST, bool PRE>
+  moe_status_t go(int waves) const {
+    const int threads = WROW ? (NC == 1 ? 1024 : 512) : 64 * waves;
+    hipLaunchKernelGGL((block_norm_bwd_kernel<EL, NC, WROW, POST, PRE>), dim3(blocks),
+                       dim3(threads), 0, s, p);
     return launch_status();
+  }
+  template <int NC, bool WROW>
+  moe_status_t run(int waves) const {
+    if (!p.y) return go<NC, WROW, false, true>(waves);
+    return p.dx ? go<NC, WROW, true, true>(waves) : go<NC, WROW, true, false>(waves);
   }
 };
 
@@ -472,7 +532,7 @@ extern "C" {
 
 moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* a, void* stream) {
   MOE_CHECK_ARG(a && a->struct_size >= sizeof(moe_block_norm_fwd_args_t));
-  MOE_CHECK_ARG(a->T >= 0 && a->d > 0 && valid_dtype(a->dtype));
+  MOE_CHECK_ARG(a->T >= 0 && a->T <= NORM_MAX_ROWS && a->d > 0 && valid_dtype(a->dtype));
   MOE_CHECK_ARG(((size_t)a->d * dtype_size(a->dtype)) % 16 == 0);
   MOE_CHECK_ARG(a->eps > 0.0f && isfinite(a->eps) && isfinite(a->res_scale));
   if (a->T == 0) return MOE_OK;
@@ -511,14 +571,17 @@ moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* a, void* stream
 
 size_t moe_block_norm_bwd_workspace_size(int T, int d) {
   if (T <= 0 || d <= 0) return 0;
-  // two partial rows per row group; up to three groups more than rows where a
-  // block holds four
-  return (size_t)(norm_groups(T) + 3) * d * 2 * sizeof(float);
+  // a row of sums per block for either norm; the larger of the two types' counts
+  // (at most NORM_MAX_CHUNKS chunks: wider rows are refused)
+  const int c16 = (int)std::min(((size_t)d + 7) / 8, (size_t)NORM_MAX_CHUNKS);
+  const int c32 = (int)std::min(((size_t)d + 3) / 4, (size_t)NORM_MAX_CHUNKS);
+  const size_t blocks = std::max(norm_bwd_blocks(T, c16), norm_bwd_blocks(T, c32));
+  return blocks * d * 2 * sizeof(float);
 }
 
 moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* a, void* stream) {
   MOE_CHECK_ARG(a && a->struct_size >= sizeof(moe_block_norm_bwd_args_t));
-  MOE_CHECK_ARG(a->T >= 0 && a->d > 0 && valid_dtype(a->dtype));
+  MOE_CHECK_ARG(a->T >= 0 && a->T <= NORM_MAX_ROWS && a->d > 0 && valid_dtype(a->dtype));
   MOE_CHECK_ARG(((size_t)a->d * dtype_size(a->dtype)) % 16 == 0);
   MOE_CHECK_ARG(a->eps > 0.0f && isfinite(a->eps) && isfinite(a->res_scale));
   const bool post = a->y != nullptr, pre = a->dx != nullptr;
@@ -539,12 +602,14 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* a, void* stream
   const bool chan_pre = a->dw_pre != nullptr, chan_post = a->dw_post || a->dgate;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float* ws = static_cast<float*>(a->ws);
-  int rows = 0;
+  const int rows = a->T > 0 ? norm_bwd_blocks(a->T, (int)chunks) : 0;
   if (a->T > 0) {
     MOE_CHECK_ARG(a->dh);
     const size_t n = (size_t)a->T * chunks * 16, nd = (size_t)a->d * 4, nt = (size_t)a->T * 4;
     const size_t need = moe_block_norm_bwd_workspace_size(a->T, a->d);
-    if ((chan_pre || chan_post) && (!ws || a->ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if ((chan_pre || chan_post) &&
+        (!ws || a->ws_bytes < need || need < (size_t)rows * a->d * 2 * sizeof(float)))
+      return MOE_ERR_WORKSPACE;
     for (void* o : {a->dh, a->dy})
       for (const void* i : {a->h1, a->y, a->dh1, a->dx}) MOE_CHECK_ARG(same_or_apart(o, i, n));
     const Span part = {chan_pre || chan_post ? ws : nullptr, need};
@@ -557,26 +622,25 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* a, void* stream
     for (const float* o : {a->dw_post, a->dgate, a->dw_pre})
       for (const void* i : {a->h1, a->y, a->dh1, a->dx}) MOE_CHECK_ARG(!overlap({o, nd}, {i, n}));
     float* part_pre = chan_pre ? ws : nullptr;
-    float* part_post = chan_post ? ws + (size_t)(norm_groups(a->T) + 3) * a->d : nullptr;
+    float* part_post = chan_post ? ws + (size_t)rows * a->d : nullptr;
     const NormBwd p = {static_cast<const u32x4*>(a->h1), static_cast<const u32x4*>(a->y),
                        static_cast<const u32x4*>(a->dh1), static_cast<const u32x4*>(a->dx),
                        a->w_post, a->gate, a->row_gate, a->w_pre, static_cast<u32x4*>(a->dh),
                        static_cast<u32x4*>(a->dy), a->drow_gate, part_pre, part_post, a->T,
                        (int)chunks, post ? a->res_scale : 1.0f, a->eps, 1.0f / (float)a->d};
     const moe_status_t st =
-        a->dtype == MOE_BF16 ? norm_dispatch((int)chunks, LaunchNormBwd<BF16>{p, s, &rows})
-                             : norm_dispatch((int)chunks, LaunchNormBwd<F32>{p, s, &rows});
+        a->dtype == MOE_BF16 ? norm_dispatch((int)chunks, LaunchNormBwd<BF16>{p, s, rows})
+                             : norm_dispatch((int)chunks, LaunchNormBwd<F32>{p, s, rows});
     if (st != MOE_OK) return st;
   }
   if (chan_pre || chan_post) {
     // no rows: exact zeros (or the existing values when accumulating)
     const float* base = rows ? ws : chan_pre ? a->w_pre : a->w_post ? a->w_post : a->gate;
     const NormFinish f = {chan_pre ? base : nullptr,
-                          chan_post ? (rows ? ws + (size_t)(norm_groups(a->T) + 3) * a->d : base)
-                                    : nullptr,
+                          chan_post ? (rows ? ws + (size_t)rows * a->d : base) : nullptr,
                           a->w_post, a->gate, a->dw_pre, a->dw_post, a->dgate, rows, a->d,
                           a->accumulate};
-    hipLaunchKernelGGL(block_norm_finish_kernel, dim3((a->d + 63) / 64, 2), dim3(1024), 0, s, f);
+    hipLaunchKernelGGL(block_norm_finish_kernel, dim3((a->d + 31) / 32, 2), dim3(1024), 0, s, f);
     return launch_status();
   }
   return MOE_OK;

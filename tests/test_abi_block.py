@@ -92,7 +92,7 @@ def test_block_norm_fwd_refusals(lib):
 def test_block_norm_bwd_refusals(lib):
     fn = lib.moe_block_norm_bwd
     need = lib.moe_block_norm_bwd_workspace_size(4, 64)
-    assert need >= 2 * 4 * 64 * 4 and lib.moe_block_norm_bwd_workspace_size(0, 64) == 0
+    assert need >= 2 * 64 * 4 and lib.moe_block_norm_bwd_workspace_size(0, 64) == 0
     a = _make(_lib.BlockNormBwdArgs, dtype=BF16, T=4, d=64, res_scale=1.0, eps=1e-6, h1=P(0), y=P(1),
               dh1=P(2), dx=P(3), w_post=P(4), gate=P(5), row_gate=P(6), w_pre=P(7), dh=P(8), dy=P(9),
               dw_post=P(10), dgate=P(11), drow_gate=P(12), dw_pre=P(13), ws=P(14), ws_bytes=need)
@@ -229,3 +229,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         ops.moe_lora_fwd(x, A, B, off, x)
     with pytest.raises(ValueError, match="accumulate"):
         ops.moe_lora_bwd(x, y, A, B, off, torch.zeros(4, 8), accumulate=True)
+
+
+def test_block_norm_workspace_covers_what_the_backward_writes(lib):
+    """At every width and many row counts the entry accepts the size its own query gives; it
+    compares that size with the partial rows it would write (without a GPU the launch
+    behind the checks is what fails; with one the entry is not called)."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    far = lambda i: (i + 1) << 36
+    for dt, q in ((BF16, 8), (F32, 4)):
+        for chunks in [*range(1, 1100, 7), 64, 65, 128, 129, 256, 257, 1024, 1025, 2048, 4096]:
+            for T in (1, 255, 257, 1025, 2500, 20000):
+                d = chunks * q
+                nb = lib.moe_block_norm_bwd_workspace_size(T, d)
+                a = _make(_lib.BlockNormBwdArgs, dtype=dt, T=T, d=d, res_scale=1.0, eps=1e-6,
+                          h1=far(0), y=far(1), dh1=far(2), dx=far(3), w_post=far(4), w_pre=far(7),
+                          dh=far(8), dy=far(9), dw_post=far(10), dw_pre=far(13), ws=far(14),
+                          ws_bytes=nb)
+                assert _status(lib.moe_block_norm_bwd, a) == _lib.MOE_ERR_HIP, (dt, d, T)
