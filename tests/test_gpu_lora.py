@@ -101,7 +101,9 @@ CASES = [(1, 64, 32, 8, 1), (1, 7168, 7168, 16, 32), (7, 96, 160, 24, 3), (64, 2
          (33, 512, 224, 40, 70), (130, 256, 352, 64, 1), (200, 1024, 96, 128, 2),
          (1027, 320, 2880, 32, 5), (700, 2048, 512, 48, 10), (515, 64, 4096, 80, 3),
          (300, 160, 128, 96, 1), (260, 128, 64, 112, 4), (40, 64, 64, 8, 1022),
-         (2048, 512, 512, 16, 1)]
+         (2048, 512, 512, 16, 1),
+         # row tiles of 64; gradients over several chunks of 1024 rows, and one adapter of most rows
+         (6200, 96, 160, 16, 2), (9000, 64, 96, 24, 3), (2300, 128, 64, 128, 2)]
 
 
 @pytest.mark.parametrize("T,K,N,r,NA", CASES)
@@ -207,6 +209,24 @@ def test_infinite_and_nan_inputs_stay_with_their_row():
     keep = [t for t in range(64) if t not in (5, 17)]
     assert torch.equal(out[keep], ref[keep])
     assert torch.isnan(out[5]).all()
+    # an infinity gives what the formula gives: ranks of zeros make 0 inf = NaN of it, ranks of
+    # one sign infinities
+    c = Case(3, 64, 64, 8, 1, ids=np.zeros(3))
+    c.A[1][:, 1:], c.B[1][:, :, 1:] = 0.0, 0.0
+    c.x[1][0], c.x[1][0, 0] = 1.0, float("inf")
+    c.A[1][0, 0] = 1.0
+    out, v = c.forward(out=torch.empty_like(c.y[1]), want_v=True)
+    assert float(v[0, 0]) == float("inf") and torch.isnan(v[0, 1:]).all()
+    assert torch.isnan(out[0]).all()
+    c.A[1].fill_(1.0)
+    b = c.B[1][0, :, 0].clone()
+    c.B[1].copy_(b[None, :, None].expand_as(c.B[1]))
+    out, v = c.forward(out=torch.empty_like(c.y[1]), want_v=True)
+    assert torch.isinf(v[0]).all()
+    assert torch.equal(out[0].float(), torch.where(b.float() > 0, float("inf"), -float("inf")))
+    _, dA, _ = c.backward(torch.zeros_like(v), want_dx=False)
+    assert not torch.isfinite(dA[0, :, 0]).any()
+    assert torch.isfinite(dA[0, :, 1:]).all()
 
 
 def test_graph_replay_with_new_plans():
