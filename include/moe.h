@@ -722,8 +722,8 @@ moe_status_t moe_clip_grad_norm(const moe_tensor_t* tensors, int n, double max_n
  *   src_row, if given, a permutation of [0, T); entries outside [0, T) are
  *     skipped.  out may be y; it overlaps nothing else.
  *   ws: moe_lora_workspace_size(T, K, N, r, NA) bytes (both directions).
- * K and N multiples of 32, r a multiple of 8 up to 128 (more:
- * MOE_ERR_UNSUPPORTED), 1 <= NA < MOE_MAX_EXPERTS. */
+ * K and N multiples of 32 up to 2^20, T up to 2^30, r a multiple of 8 up to 128
+ * (more: MOE_ERR_UNSUPPORTED), 1 <= NA < MOE_MAX_EXPERTS. */
 typedef struct {
   size_t struct_size; /* = sizeof(moe_lora_fwd_args_t) */
   int dtype;

@@ -95,6 +95,30 @@ __device__ __forceinline__ float rest_of(float v, uint32_t b) {
   return h == v ? 0.0f : v - h;
 }
 
+// Four values' high and low bf16 parts.
+__device__ __forceinline__ void split_quad(const f32x4& v, u32x2& hi, u32x2& lo) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t h0 = bf16_of(v[2 * q]), h1 = bf16_of(v[2 * q + 1]);
+    hi[q] = h0 | h1 << 16;
+    lo[q] = bf16_of(rest_of(v[2 * q], h0)) | bf16_of(rest_of(v[2 * q + 1], h1)) << 16;
+  }
+}
+
+// Eight bf16 values plus eight float32 ones, rounded once.
+__device__ __forceinline__ u32x4 add_chunk(const u32x4& y, const f32x4& a, const f32x4& b) {
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  float v[8];
+  unpack_chunk(y, v, BF16());
+  f32x8 f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e] = v[e] + a[e];
+    f[e + 4] = v[e + 4] + b[e];
+  }
+  return __builtin_bit_cast(u32x4, __builtin_convertvector(f, bf16x8));
+}
+
 // The 4 x 16 block that a group of 16 lanes reads with ds_read_b64_tr_b16: lane
 // 4 q + r addresses four elements of row q, lane i receives rows 0 .. 3 of
 // element i & 3 of the segment that lanes r = i >> 2 address.
@@ -110,102 +134,145 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Eight elements of a column of w (row stride ld), rows i .. i + 7.
-__device__ __forceinline__ u32x4 column8(const uint16_t* w, size_t ld) {
-  u32x4 o;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    o[q] = (uint32_t)w[(2 * q) * ld] | ((uint32_t)w[(2 * q + 1) * ld] << 16);
-  return o;
-}
-
 struct LoraShrink {
   const uint16_t *x, *w;      // rows [T, C]; factor [NA, r, C], or [NA, C, r] (TRANS)
   const int32_t *offsets, *src_row;
   float* part;                // [splits][T][r], by position
-  int T, C, r, NA, steps;     // steps of 32 along C
+  int T, C, r, NA, chunks, splits;    // chunks of KC along C
 };
 
 // part[split][p][j] = sum over the split's share of C of x[t(p)][c] w[a][j][c].
-// The four waves share the block's steps; MFMA: first operand the factor's rows
-// (register 4 (lane >> 4) + q = rank), second the activation rows (lane & 15).
+// The waves share the block's chunks of KC columns.  A wave stages its chunk of
+// the rows and of the factor through LDS of its own: whole lines are loaded
+// (KC / 8 lanes a row) while the chunk before is multiplied; loading MFMA
+// fragments straight from memory, 16 bytes from each of 16 rows at a time, kept
+// the address units busier than the memory.  MFMA: first operand the factor's
+// rows (register 4 (lane >> 4) + q = rank), second the activation rows
+// (lane & 15).  A factor whose reduction runs over its rows (TRANS) is read
+// transposed.
 template <int MT, int RT, bool TRANS>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_shrink_kernel(const LoraShrink p) {
   constexpr int TM = 16 * MT, R = 16 * RT;
-  constexpr int U = RT <= 2 ? 4 : 2;        // steps whose loads are in flight together
-  __shared__ float red[LORA_WAVES][16][R + 4];
-  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, TM, blockIdx.x);
+  constexpr int KC = RT <= 4 ? 64 : 32;
+  constexpr int LPR = KC / 8;                // lanes per row of a chunk
+  constexpr int RPI = 64 / LPR;              // rows per load instruction
+  constexpr int NX = TM / RPI, NW = R * KC / 512;   // load instructions per chunk
+  constexpr int XS = KC + 8;                 // row strides in LDS, elements
+  constexpr int WS = TRANS ? R + 8 : KC + 8, WROWS = TRANS ? KC : R;
+  __shared__ __align__(16) uint16_t xs[LORA_WAVES][TM][XS];
+  __shared__ __align__(16) uint16_t wt[LORA_WAVES][WROWS][WS];
+  __shared__ __align__(16) float red[LORA_WAVES][16][16 + 4];
+  const int split = blockIdx.x % p.splits;
+  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, TM, blockIdx.x / p.splits);
   if (tl.n <= 0 || tl.a >= p.NA) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & 15, g = lane >> 4;
-  // rows past the tile, ranks past r: a valid row or rank is read again, its
-  // results are dropped
-  const uint16_t* xr[MT];
+  const int lr = lane / LPR, lc = 8 * (lane % LPR);
+  // rows past the tile read a valid row again, their results are dropped
+  const uint16_t* xr[NX];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = lora_token(p.src_row, tl.p0 + min(16 * m + l, tl.n - 1), p.T);
-    xr[m] = p.x + (size_t)max(t, 0) * p.C + 8 * g;
+  for (int i = 0; i < NX; ++i) {
+    const int t = lora_token(p.src_row, tl.p0 + min(RPI * i + lr, tl.n - 1), p.T);
+    xr[i] = p.x + (size_t)max(t, 0) * p.C + lc;
   }
   const uint16_t* w = p.w + (size_t)tl.a * p.r * p.C;
-  f32x4 acc[MT][RT] = {};
-  const int parts = gridDim.y * LORA_WAVES, part = blockIdx.y * LORA_WAVES + wave;
-  const int s0 = (int)((long long)p.steps * part / parts);
-  const int s1 = (int)((long long)p.steps * (part + 1) / parts);
-  auto load = [&](int s, u32x4 (&xa)[MT], u32x4 (&wa)[RT]) {
+  // TRANS: the factor's chunk is KC r consecutive elements, 16 bytes a lane and
+  // instruction; where each lands
+  int wo[NW], wd[NW];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xa[m] = *reinterpret_cast<const u32x4*>(xr[m] + 32 * s);
+  for (int i = 0; i < NW; ++i) {
+    if constexpr (TRANS) {
+      const int per = p.r / 8, k = 64 * i + lane, row = k / per;
+      wo[i] = k < KC * per ? 8 * k : -1;
+      wd[i] = row * WS + 8 * (k - row * per);
+    } else {
+      // ranks past r read the last one again, their results are dropped
+      wo[i] = min(RPI * i + lr, p.r - 1) * p.C + lc;
+      wd[i] = (RPI * i + lr) * WS + lc;
+    }
+  }
+  // Every load is issued (past C: the last columns again), so that the compiler can
+  // count the ones in flight; what lies past C becomes zero on its way to LDS.
+  const u32x4 zero = {0, 0, 0, 0};
+  u32x4 xa[NX], wa[NW];
+  auto fetch = [&](int s) {
+    const int col = min(KC * s, p.C - 8 - lc);
+#pragma unroll
+    for (int i = 0; i < NX; ++i) xa[i] = *reinterpret_cast<const u32x4*>(xr[i] + col);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if constexpr (TRANS)
+        wa[i] = *reinterpret_cast<const u32x4*>(w + min(KC * s * p.r + max(wo[i], 0), p.C * p.r - 8));
+      else
+        wa[i] = *reinterpret_cast<const u32x4*>(w + wo[i] + col);
+    }
+  };
+  f32x4 acc[MT][RT] = {};
+  // the waves of all splits of a tile (neighbours in the grid) take the chunks in
+  // turn, so that together they walk the rows' lines in order
+  const int stride = p.splits * LORA_WAVES, s0 = split * LORA_WAVES + wave;
+  fetch(min(s0, p.chunks - 1));
+  for (int s = s0; s < p.chunks; s += stride) {
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      *reinterpret_cast<u32x4*>(&xs[wave][RPI * i + lr][lc]) = KC * s + lc < p.C ? xa[i] : zero;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const bool in = TRANS ? KC * s * p.r + wo[i] < p.C * p.r : KC * s + lc < p.C;
+      if (!TRANS || wo[i] >= 0)
+        *reinterpret_cast<u32x4*>(&wt[wave][0][0] + wd[i]) = in ? wa[i] : zero;
+    }
+    wave_fence();
+    fetch(min(s + stride, p.chunks - 1));
+#pragma unroll
+    for (int k = 0; k < KC; k += 32) {
+      u32x4 xf[MT], wf[RT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        xf[m] = *reinterpret_cast<const u32x4*>(&xs[wave][16 * m + l][k + 8 * g]);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        if constexpr (TRANS) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x2 v =
+                read_tr(&wt[wave][k + 8 * g + 4 * h + (l >> 2)][16 * j + 4 * (l & 3)]);
+            wf[j][2 * h] = v[0];
+            wf[j][2 * h + 1] = v[1];
+          }
+        } else {
+          wf[j] = *reinterpret_cast<const u32x4*>(&wt[wave][16 * j + l][k + 8 * g]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[m][j] = mfma16(wf[j], xf[m], acc[m][j]);
+    }
+  }
+  // the waves' sums, in wave order, 16 rows and ranks at a time
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int rank = min(16 * j + l, p.r - 1);
-      if constexpr (TRANS)
-        wa[j] = column8(w + (size_t)(32 * s + 8 * g) * p.r + rank, p.r);
-      else
-        wa[j] = *reinterpret_cast<const u32x4*>(w + (size_t)rank * p.C + 32 * s + 8 * g);
-    }
-  };
-  auto mma = [&](const u32x4 (&xa)[MT], const u32x4 (&wa)[RT]) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[m][j] = mfma16(wa[j], xa[m], acc[m][j]);
-  };
-  int s = s0;
-  for (; s + U <= s1; s += U) {
-    u32x4 xa[U][MT], wa[U][RT];
-#pragma unroll
-    for (int k = 0; k < U; ++k) load(s + k, xa[k], wa[k]);
-#pragma unroll
-    for (int k = 0; k < U; ++k) mma(xa[k], wa[k]);
-  }
-  for (; s < s1; ++s) {
-    u32x4 xa[MT], wa[RT];
-    load(s, xa, wa);
-    mma(xa, wa);
-  }
-  // the waves' sums, in wave order, 16 rows at a time
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m) __syncthreads();
-#pragma unroll
-    for (int j = 0; j < RT; ++j)
-      *reinterpret_cast<f32x4*>(&red[wave][l][16 * j + 4 * g]) = acc[m][j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * R / 4; i += 64 * LORA_WAVES) {
-      const int row = i / (R / 4), c = i % (R / 4) * 4;
-      if (16 * m + row < tl.n && c < p.r) {
+      if (m || j) __syncthreads();
+      *reinterpret_cast<f32x4*>(&red[wave][l][4 * g]) = acc[m][j];
+      __syncthreads();
+      const int row = threadIdx.x >> 2, c = 4 * (threadIdx.x & 3);
+      if (threadIdx.x < 64 && 16 * m + row < tl.n && 16 * j + c < p.r) {
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < LORA_WAVES; ++k) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(&red[k][row][c]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += o[q];
-        }
-        *reinterpret_cast<f32x4*>(p.part + ((size_t)blockIdx.y * p.T + tl.p0 + 16 * m + row) * p.r +
-                                  c) = v;
+        for (int k = 0; k < LORA_WAVES; ++k) v += *reinterpret_cast<const f32x4*>(&red[k][row][c]);
+        *reinterpret_cast<f32x4*>(p.part + ((size_t)split * p.T + tl.p0 + 16 * m + row) * p.r +
+                                  16 * j + c) = v;
       }
     }
-  }
 }
+
+// The first of the four columns, within a wave's 64, that lane group g holds of
+// MFMA tile i.
+__device__ __forceinline__ int lora_column(int i, int g) { return 32 * (i >> 1) + 8 * g + 4 * (i & 1); }
 
 struct LoraExpand {
   const float* part;          // [splits][T][r]
@@ -216,13 +283,14 @@ struct LoraExpand {
   uint16_t* out;              // [T, C] or NULL (only v_out is wanted); may be y
   float* v_out;               // [T, r] or NULL: the added parts
   int T, C, r, NA, splits, scale_v;   // scale_v: v_out holds s[a] v
+  int col_blocks;
 };
 
 // out[t(p)][c] = y + sum_j s[a] v[p][j] w[a][c][j].  A wave takes chunks of 64
 // columns of the tile's rows, the next chunk's y loaded meanwhile: its four MFMA
-// tiles hold columns 16 g + 4 i + q of lane group g (tile i, register q), so a
-// lane ends up with 16 consecutive columns of its row: 32-byte loads of y and
-// stores of out, whole 128-byte lines per row.  A factor stored the other way
+// tiles hold columns 32 (i / 2) + 8 g + 4 (i % 2) + q of lane group g (tile i,
+// register q), so a lane ends up with two runs of 8 columns of its row and each
+// load of y and store of out covers 64 contiguous bytes of 16 rows.  A factor stored the other way
 // (TRANS) passes through LDS and is read transposed.
 template <int MT, int RT, bool TRANS>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const LoraExpand p) {
@@ -231,12 +299,13 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
   constexpr int WS = 64 + 8;                // row stride of a wave's factor tile
   __shared__ __align__(16) uint16_t vs[TM][KP + 8];
   __shared__ __align__(16) uint16_t wt[TRANS ? LORA_WAVES : 1][TRANS ? R : 1][WS];
-  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, TM, blockIdx.x);
+  const int cb = blockIdx.x % p.col_blocks;
+  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, TM, blockIdx.x / p.col_blocks);
   if (tl.n <= 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & 15, g = lane >> 4;
-  const int chunks = (p.C + 63) / 64, step = gridDim.y * LORA_WAVES;
-  int ch = blockIdx.y * LORA_WAVES + wave;
+  const int chunks = (p.C + 63) / 64, step = p.col_blocks * LORA_WAVES;
+  int ch = cb * LORA_WAVES + wave;
   const u32x4 zero = {0, 0, 0, 0};
   if (tl.a >= p.NA) {                       // no adapter: the rows as they are
     if (!p.out || p.out == p.y) return;
@@ -258,13 +327,13 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
     t[m] = 16 * m + l < tl.n ? lora_token(p.src_row, tl.p0 + 16 * m + l, p.T) : -1;
   u32x4 yr[MT][2];
   auto fetch = [&](int chunk) {
-    const int c = 64 * chunk + 16 * g;
+    const int c = 64 * chunk + 8 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        yr[m][q] = p.y && p.out && t[m] >= 0 && c < p.C
-                       ? reinterpret_cast<const u32x4*>(p.y + (size_t)t[m] * p.C + c)[q]
+        yr[m][q] = p.y && p.out && t[m] >= 0 && c + 32 * q < p.C
+                       ? *reinterpret_cast<const u32x4*>(p.y + (size_t)t[m] * p.C + c + 32 * q)
                        : zero;
   };
   fetch(ch);
@@ -287,17 +356,12 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
       }
       for (; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
       const f32x4 sv = v * sc;
-      if (p.v_out && blockIdx.y == 0)
+      if (p.v_out && cb == 0)
         *reinterpret_cast<f32x4*>(p.v_out + (size_t)(tl.p0 + row) * p.r + j) = p.scale_v ? sv : v;
       v = sv;
     }
     u32x2 hi, lo;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t h0 = bf16_of(v[2 * q]), h1 = bf16_of(v[2 * q + 1]);
-      hi[q] = h0 | h1 << 16;
-      lo[q] = bf16_of(rest_of(v[2 * q], h0)) | bf16_of(rest_of(v[2 * q + 1], h1)) << 16;
-    }
+    split_quad(v, hi, lo);
     *reinterpret_cast<u32x2*>(&vs[row][j]) = hi;
     *reinterpret_cast<u32x2*>(&vs[row][p.r + j]) = lo;
   }
@@ -315,7 +379,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 2; ++q) yc[m][q] = yr[m][q];
-    if (ch + step < chunks) fetch(ch + step);
+    // Loads return in order, so the next chunk's y is asked for behind the
+    // factor's loads of this one: waiting for those does not wait for it.
     if constexpr (TRANS) {
       // eight rows of 128 bytes per instruction
       u32x4 raw[2 * RT];
@@ -324,6 +389,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
       for (int i = 0; i < 2 * RT; ++i)
         raw[i] = *reinterpret_cast<const u32x4*>(
             w + (size_t)min(8 * i + (lane >> 3), p.r - 1) * p.C + c);
+      if (ch + step < chunks) fetch(ch + step);
       wave_fence();
 #pragma unroll
       for (int i = 0; i < 2 * RT; ++i)
@@ -340,15 +406,16 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
         if constexpr (TRANS) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const u32x2 v = read_tr(&wt[wave][j + 4 * h + (l >> 2)][16 * (l & 3) + 4 * i]);
+            const u32x2 v = read_tr(&wt[wave][j + 4 * h + (l >> 2)][lora_column(i, l & 3)]);
             wa[i][2 * h] = v[0];
             wa[i][2 * h + 1] = v[1];
           }
         } else {
-          const int c = min(64 * ch + 16 * (l >> 2) + 4 * i + (l & 3), p.C - 1);
+          const int c = min(64 * ch + lora_column(i, l >> 2) + (l & 3), p.C - 1);
           wa[i] = *reinterpret_cast<const u32x4*>(w + (size_t)c * p.r + j);
         }
       }
+      if (!TRANS && s == ksteps - 1 && ch + step < chunks) fetch(ch + step);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const u32x4 va = *reinterpret_cast<const u32x4*>(&vs[16 * m + l][32 * s + 8 * g]);
@@ -356,24 +423,217 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
         for (int i = 0; i < 4; ++i) acc[m][i] = mfma16(wa[i], va, acc[m][i]);
       }
     }
-    const int c = 64 * ch + 16 * g;
-    if (c >= p.C) continue;
+    const int c = 64 * ch + 8 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (t[m] < 0) continue;
-      const size_t o = (size_t)t[m] * p.C + c;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        typedef float f32x8 __attribute__((ext_vector_type(8)));
-        float v[8];
-        unpack_chunk(yc[m][q], v, BF16());
-        f32x8 f;
+      for (int q = 0; q < 2; ++q)
+        if (c + 32 * q < p.C)
+          *reinterpret_cast<u32x4*>(p.out + (size_t)t[m] * p.C + c + 32 * q) =
+              add_chunk(yc[m][q], acc[m][2 * q], acc[m][2 * q + 1]);
+    }
+  }
+}
+
+// The rank values of all rows between shrink and apply: the splits' parts added
+// in order and split into two bf16 parts, each padded to KH 32-rank steps with
+// zeros: pk[p][hi or lo][32 KH].
+struct LoraPack {
+  const float* part;
+  const float* scale;
+  const int32_t* offsets;
+  uint16_t* pk;
+  float* v_out;
+  int T, r, NA, splits, scale_v, kh;
+};
+
+static constexpr int PACK_ROWS = 32;
+
+__global__ void __launch_bounds__(256) lora_pack_kernel(const LoraPack p) {
+  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, PACK_ROWS, blockIdx.x);
+  if (tl.n <= 0 || tl.a >= p.NA) return;
+  const float sc = p.scale ? p.scale[tl.a] : 1.0f;
+  const int quads = 8 * p.kh;               // of a padded row
+  for (int i = threadIdx.x; i < tl.n * quads; i += 256) {
+    const int row = i / quads, j = (i - row * quads) * 4;
+    const size_t pos = tl.p0 + row;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (j < p.r) {
+      const float* src = p.part + pos * p.r + j;
+      const size_t ld = (size_t)p.T * p.r;
+      for (int k = 0; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
+      const f32x4 sv = v * sc;
+      if (p.v_out) *reinterpret_cast<f32x4*>(p.v_out + pos * p.r + j) = p.scale_v ? sv : v;
+      v = sv;
+    }
+    u32x2 hi, lo;
+    split_quad(v, hi, lo);
+    uint16_t* o = p.pk + pos * (64 * p.kh) + j;
+    *reinterpret_cast<u32x2*>(o) = hi;
+    *reinterpret_cast<u32x2*>(o + 32 * p.kh) = lo;
+  }
+}
+
+struct LoraApply {
+  const uint16_t* pk;
+  const uint16_t* w;          // factor [NA, C, r], or [NA, r, C] (TRANS)
+  const int32_t *offsets, *src_row;
+  const uint16_t* y;          // [T, C] or NULL (zeros)
+  uint16_t* out;              // [T, C], may be y
+  int T, C, r, NA, rows;      // rows of one adapter that a block takes
+  unsigned col_blocks;
+};
+
+static constexpr int APPLY_ROWS = 512;      // at most
+
+// expand for many rows: a wave keeps the factor of its 64 columns in registers
+// and walks its block's rows 16 at a time, the loads of the next DEPTH steps in
+// flight, so the factor is read once per block of rows and nothing but the
+// rows moves in the loop.  Columns are placed as in lora_expand_kernel.
+//
+// What bounds it is how the memory is walked, measured with plain copies of
+// 8192 x 8192 bytes cut the same way: 64 bytes of 16 rows an instruction
+// 3.3 TB/s, 128 bytes of 8 rows 3.6, with the blocks of the same rows next to
+// each other in the grid 5.0, with nontemporal stores 6.5.  So the column blocks
+// come first in the grid, the outputs (far larger than the L2) are stored
+// nontemporally, and two lanes that hold halves of two rows (l and l ^ 8)
+// swap chunks, so that an instruction covers whole 128-byte lines of 8 rows.
+//
+// The loop over whole steps has no branch and no mask (a step past the last one
+// loads the last one again): behind a load that may not have been issued the
+// compiler can only wait for everything, stores included, which emptied the
+// pipeline every round.  Ragged ends, rows without a source and columns past C
+// take a plain loop.
+template <int KH, bool TRANS>
+__global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraApply p) {
+  constexpr int DEPTH = KH <= 2 ? 4 : 2;
+  __shared__ int toks[APPLY_ROWS];
+  const LoraTile tl =
+      lora_tile<false>(p.offsets, p.NA, p.T, p.rows, (int)(blockIdx.x / p.col_blocks));
+  if (tl.n <= 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l = lane & 15, g = lane >> 4;
+  const int c0 = (int)(blockIdx.x % p.col_blocks * LORA_WAVES + wave) * 64, c = c0 + 8 * g;
+  if (tl.a >= p.NA) {                       // no adapter: the rows as they are
+    if (p.out == p.y) return;
+    const u32x4 zero = {0, 0, 0, 0};
+    const int cc = c0 + 8 * (lane & 7);
+    for (int i = lane >> 3; i < tl.n; i += 8) {
+      const int t = lora_token(p.src_row, tl.p0 + i, p.T);
+      if (t < 0 || cc >= p.C) continue;
+      const size_t o = (size_t)t * p.C + cc;
+      *reinterpret_cast<u32x4*>(p.out + o) = p.y ? *reinterpret_cast<const u32x4*>(p.y + o) : zero;
+    }
+    return;
+  }
+  int bad = 0;
+  for (int i = threadIdx.x; i < p.rows; i += 64 * LORA_WAVES) {
+    const int t = i < tl.n ? lora_token(p.src_row, tl.p0 + i, p.T) : -1;
+    bad |= i < tl.n && t < 0;
+    toks[i] = t;
+  }
+  u32x4 wa[KH][4];
+  const uint16_t* w = p.w + (size_t)tl.a * p.r * p.C;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[e] + acc[m][2 * q + e / 4][e % 4];
-        reinterpret_cast<u32x4*>(p.out + o)[q] =
-            __builtin_bit_cast(u32x4, __builtin_convertvector(f, bf16x8));
+  for (int s = 0; s < KH; ++s) {
+    const int j = 32 * s + 8 * g < p.r ? 32 * s + 8 * g : 0;     // past r the rank values are zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int cw = min(c0 + lora_column(i, l >> 2) + (l & 3), p.C - 1);
+      if constexpr (TRANS) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          wa[s][i][q] = (uint32_t)w[(size_t)(j + 2 * q) * p.C + cw] |
+                        (uint32_t)w[(size_t)(j + 2 * q + 1) * p.C + cw] << 16;
+      } else {
+        wa[s][i] = *reinterpret_cast<const u32x4*>(w + (size_t)cw * p.r + j);
       }
     }
+  }
+  const bool plain = __syncthreads_or(bad) || !p.y || c0 + 64 > p.C;
+  const uint16_t* pk = p.pk + (size_t)tl.p0 * (64 * KH) + 8 * g;
+  auto load_v = [&](int row, u32x4 (&v)[2 * KH]) {
+#pragma unroll
+    for (int k = 0; k < 2 * KH; ++k)
+      v[k] = *reinterpret_cast<const u32x4*>(pk + (size_t)row * (64 * KH) + 32 * k);
+  };
+  auto add = [&](const u32x4 (&v)[2 * KH], const u32x4* y, u32x4* o) {
+    f32x4 acc[4] = {};
+#pragma unroll
+    for (int k = 0; k < 2 * KH; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = mfma16(wa[k % KH][i], v[k], acc[i]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) o[q] = add_chunk(y[q], acc[2 * q], acc[2 * q + 1]);
+  };
+  int s = 0;
+  const int whole = plain ? 0 : tl.n / 16 / DEPTH * DEPTH;
+  if (whole > 0) {
+    u32x4 yr[DEPTH][2], vr[DEPTH][2 * KH];
+    uint16_t* at[DEPTH][2];
+    // instruction q: rows 8 q + (l & 7), chunk 4 (l >> 3) + g of the 128 bytes
+    const int col = c0 + 32 * (l >> 3) + 8 * g;
+    auto fetch = [&](int d, int step) {
+      const int row = 16 * min(step, whole - 1);
+      load_v(row + l, vr[d]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const size_t o = (size_t)toks[row + 8 * q + (l & 7)] * p.C + col;
+        at[d][q] = p.out + o;
+        yr[d][q] = *reinterpret_cast<const u32x4*>(p.y + o);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // lanes l < 8 give their second chunk for the first of lane l + 8 (its own inverse)
+    auto swap = [&](u32x4* v) {
+      const u32x4 give = l < 8 ? v[1] : v[0];
+      u32x4 got;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)          // row_ror:8: lane l ^ 8 of each 16
+        got[i] = __builtin_amdgcn_update_dpp(0, (int)give[i], 0x128, 0xf, 0xf, false);
+      if (l < 8) v[1] = got;
+      else v[0] = got;
+    };
+    auto round = [&]() {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        u32x4 o[2];
+        swap(yr[d]);
+        add(vr[d], yr[d], o);
+        swap(o);
+        uint16_t* to[2] = {at[d][0], at[d][1]};
+        fetch(d, s + DEPTH + d);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          __builtin_nontemporal_store(o[q], reinterpret_cast<u32x4*>(to[q]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      s += DEPTH;
+    };
+    // The loads in order (the scheduling barriers), and the first round apart, so
+    // that the loop is entered with the same accesses in flight as it repeats with.
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) fetch(d, d);
+    round();
+    while (s < whole) round();
+  }
+  for (; 16 * s < tl.n; ++s) {
+    const int t = toks[16 * s + l];
+    u32x4 y[2], v[2 * KH], o[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const u32x4 zero = {0, 0, 0, 0};
+      y[q] = t >= 0 && p.y && c + 32 * q < p.C
+                 ? *reinterpret_cast<const u32x4*>(p.y + (size_t)t * p.C + c + 32 * q)
+                 : zero;
+    }
+    load_v(min(16 * s + l, tl.n - 1), v);
+    add(v, y, o);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (t >= 0 && c + 32 * q < p.C)
+        *reinterpret_cast<u32x4*>(p.out + (size_t)t * p.C + c + 32 * q) = o[q];
   }
 }
 
@@ -411,9 +671,9 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][XS];
   __shared__ float red[LORA_WAVES][16][64 + 4];
   const LoraGrad& G = p.g[blockIdx.z];
-  const int c0 = blockIdx.y * 64;
+  const int c0 = blockIdx.x * 64;
   if (!G.out || c0 >= G.C) return;
-  const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.x);
+  const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.y);
   if (tl.n < 0 || tl.a >= p.NA) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & 15, g = lane >> 4;
@@ -421,29 +681,45 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   // the tokens of 32 rows, one a lane (both halves of the wave alike)
   auto tokens = [&](int s) {
     const int i = 32 * s + (lane & 31);
-    return i < tl.n ? lora_token(p.src_row, tl.p0 + i, p.T) : -1;
+    const int t = lora_token(p.src_row, tl.p0 + min(i, tl.n - 1), p.T);
+    return i < tl.n ? t : -1;
   };
   const u32x4 zero = {0, 0, 0, 0};
+  // (every load is issued, rows without a token read row 0 and become zero on
+  // their way to LDS: the compiler can then count the loads in flight)
   auto fetch = [&](int tok, u32x4 (&x)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = __shfl(tok, 8 * i + (lane >> 3), 64);
-      x[i] = t >= 0 ? *reinterpret_cast<const u32x4*>(G.x + (size_t)t * G.C + xc) : zero;
+      x[i] = *reinterpret_cast<const u32x4*>(G.x + (size_t)max(t, 0) * G.C + xc);
     }
   };
   f32x4 acc[RT][4] = {};
   const int steps = (tl.n + 31) / 32;
-  int tok = tokens(wave);
   u32x4 x[4];
-  fetch(tok, x);
-  int next = tokens(wave + LORA_WAVES);
+  int tok = -1, next = -1;
+  if (wave < steps) {           // (an adapter without rows reads nothing)
+    tok = tokens(wave);
+    fetch(tok, x);
+    next = tokens(wave + LORA_WAVES);
+  }
   for (int s = wave; s < steps; s += LORA_WAVES) {
     const uint32_t valid = (uint32_t)__ballot(tok >= 0);
     wave_fence();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x4*>(&xs[wave][8 * i + (lane >> 3)][8 * (lane & 7)]) = x[i];
+      *reinterpret_cast<u32x4*>(&xs[wave][8 * i + (lane >> 3)][8 * (lane & 7)]) =
+          valid >> (8 * i + (lane >> 3)) & 1 ? x[i] : zero;
     wave_fence();
+    // (u's loads in front of the next rows': loads return in order)
+    const float* u = G.u + (size_t)(tl.p0 + 32 * s) * p.r;
+    const int last = tl.n - 1 - 32 * s;
+    float uv[RT][8];
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(16 * j + l, p.r - 1)];
     tok = next;
     fetch(tok, x);
     next = tokens(s + 2 * LORA_WAVES);
@@ -456,18 +732,15 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
         xa[i][2 * h] = v[0];
         xa[i][2 * h + 1] = v[1];
       }
-    const float* u = G.u + (size_t)(tl.p0 + 32 * s + 8 * g) * p.r;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int rank = 16 * j + l;
       u32x4 part[3];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t b[3][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = 2 * q + e;
-          float v = rank < p.r && (valid >> (8 * g + row) & 1) ? u[(size_t)row * p.r + rank] : 0.0f;
+          float v = 16 * j + l < p.r && (valid >> (8 * g + 2 * q + e) & 1) ? uv[j][2 * q + e] : 0.0f;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             b[k][e] = bf16_of(v);
@@ -527,32 +800,40 @@ __global__ void __launch_bounds__(256) lora_wgrad_sum_kernel(const LoraWgrad p) 
   *o = p.accumulate ? *o + v : v;
 }
 
-// Row tiles of 16, 32 or 64: the highest that the adapters fill on average and
-// that still gives 96 tiles (a factor's tile is read once per tile of rows,
-// while few tiles leave the card empty or cost splits of the reduction).
-static int lora_mt(int T, int NA) {
+// Row tiles of 16, 32 or 64.  A factor's tile is read once per tile of rows, so
+// the highest tile that the adapters fill on average is taken, as long as it
+// leaves `least` tiles.  Shrink, whose tiles are its blocks, asks for 192 (below,
+// it splits the reduction); expand, which has the columns to spread over, for
+// 256 tiles x 256 columns.
+static int lora_mt(int T, int NA, int least) {
   for (int mt = 4; mt > 1; mt /= 2)
-    if (T >= 16 * mt * std::max(NA, 96)) return mt;
+    if (T >= 16 * mt * std::max(NA, least)) return mt;
   return 1;
 }
+static int shrink_mt(int T, int NA) { return lora_mt(T, NA, 192); }
+static int expand_mt(int T, int NA, int C) { return lora_mt(T, NA, std::max(1, 256 * 256 / C)); }
 static int lora_tiles(int T, int NA, int mt) { return T / (16 * mt) + std::min(NA + 1, T) + 1; }
 
-// Blocks along a reduction of `steps` steps: enough tiles x splits to fill the
-// card twice, with at least two steps per wave.
-static int lora_splits(int T, int NA, int mt, int steps) {
+static int lora_rank_tiles(int r) { return r <= 64 ? (r + 15) / 16 : r <= 96 ? 6 : 8; }
+// Chunks of the reduction over C (as lora_shrink_kernel cuts it).
+static int lora_chunks(int C, int r) { return lora_rank_tiles(r) <= 4 ? (C + 63) / 64 : C / 32; }
+
+// Blocks along a reduction: as many as fill the card, with at least two chunks
+// per wave.
+static int lora_splits(int T, int NA, int C, int r) {
+  const int mt = shrink_mt(T, NA);
   const int tiles = std::max(1, T / (16 * mt) + (mt == 1 ? std::min(NA, T) / 2 : 0));
-  return std::max(1, std::min({512 / tiles, steps / (2 * LORA_WAVES), 16}));
+  return std::max(1, std::min({512 / tiles, lora_chunks(C, r) / (2 * LORA_WAVES), 16}));
 }
 
 // Calls f(RT) for the rank tiles that cover r (1, 2, 3, 4, 6 or 8 of 16).
 template <class F>
 static moe_status_t lora_ranks(int r, F&& f) {
-  switch ((r + 15) / 16) {
+  switch (lora_rank_tiles(r)) {
     case 1: f(std::integral_constant<int, 1>()); break;
     case 2: f(std::integral_constant<int, 2>()); break;
     case 3: f(std::integral_constant<int, 3>()); break;
     case 4: f(std::integral_constant<int, 4>()); break;
-    case 5:
     case 6: f(std::integral_constant<int, 6>()); break;
     default: f(std::integral_constant<int, 8>()); break;
   }
@@ -560,8 +841,11 @@ static moe_status_t lora_ranks(int r, F&& f) {
 }
 
 template <bool TRANS>
-static moe_status_t launch_shrink(const LoraShrink& p, int mt, int splits, hipStream_t s) {
-  const dim3 grid(lora_tiles(p.T, p.NA, mt), splits), block(64 * LORA_WAVES);
+static moe_status_t launch_shrink(const LoraShrink& p, hipStream_t s) {
+  const int mt = shrink_mt(p.T, p.NA);
+  const size_t blocks = (size_t)lora_tiles(p.T, p.NA, mt) * p.splits;
+  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
   return lora_ranks(p.r, [&](auto N) {
     constexpr int RT = decltype(N)::value;
     if (mt == 4) hipLaunchKernelGGL((lora_shrink_kernel<4, RT, TRANS>), grid, block, 0, s, p);
@@ -571,18 +855,59 @@ static moe_status_t launch_shrink(const LoraShrink& p, int mt, int splits, hipSt
 }
 
 template <bool TRANS>
-static moe_status_t launch_expand(const LoraExpand& p, int mt, hipStream_t s) {
+static moe_status_t launch_expand(LoraExpand p, hipStream_t s) {
+  const int mt = expand_mt(p.T, p.NA, p.C);
   // blocks along the columns: one per 256 columns, fewer (each then walks several
-  // chunks and reads the tile's ranks once) as long as 1024 blocks remain
+  // chunks and reads the tile's ranks once) as long as the card is filled
+  const int fill = mt == 1 ? 1024 : 512;
   const int tiles = lora_tiles(p.T, p.NA, mt), cols = (p.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
-  const int by = p.out ? std::min(cols, std::max(1, (1024 + tiles - 1) / tiles)) : 1;
-  const dim3 grid(tiles, by), block(64 * LORA_WAVES);
+  p.col_blocks = p.out ? std::min(cols, std::max(1, fill / tiles)) : 1;
+  const size_t blocks = (size_t)tiles * p.col_blocks;
+  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
   return lora_ranks(p.r, [&](auto N) {
     constexpr int RT = decltype(N)::value;
     if (mt == 4) hipLaunchKernelGGL((lora_expand_kernel<4, RT, TRANS>), grid, block, 0, s, p);
     else if (mt == 2) hipLaunchKernelGGL((lora_expand_kernel<2, RT, TRANS>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((lora_expand_kernel<1, RT, TRANS>), grid, block, 0, s, p);
   });
+}
+
+// Many rows: pack and apply in place of expand.  They cost a launch more, and
+// pay from about 16 MiB of output on.
+static bool lora_apply(int T, int C) { return (size_t)T * C >= (8u << 20); }
+static int lora_kh(int r) { return (r + 31) / 32; }
+
+template <bool TRANS>
+static moe_status_t launch_apply(const LoraExpand& e, uint16_t* pk, hipStream_t s) {
+  const int kh = lora_kh(e.r);
+  const LoraPack pp = {e.part, e.scale, e.offsets, pk, e.v_out, e.T, e.r, e.NA, e.splits, e.scale_v,
+                       kh};
+  hipLaunchKernelGGL(lora_pack_kernel, dim3(e.T / PACK_ROWS + std::min(e.NA + 1, e.T) + 1), dim3(256),
+                     0, s, pp);
+  moe_status_t st = launch_status();
+  if (st != MOE_OK) return st;
+  const int cols = (e.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
+  // rows a block: about 640 blocks
+  const int rows = std::max(64, std::min(APPLY_ROWS, (int)((size_t)e.T * cols / 640) / 16 * 16));
+  const LoraApply pa = {pk, e.w, e.offsets, e.src_row, e.y, e.out, e.T, e.C, e.r, e.NA, rows,
+                        (unsigned)cols};
+  const size_t blocks = (size_t)(e.T / rows + std::min(e.NA + 1, e.T) + 1) * cols;
+  if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
+  switch (kh) {
+    case 1: hipLaunchKernelGGL((lora_apply_kernel<1, TRANS>), grid, block, 0, s, pa); break;
+    case 2: hipLaunchKernelGGL((lora_apply_kernel<2, TRANS>), grid, block, 0, s, pa); break;
+    case 3: hipLaunchKernelGGL((lora_apply_kernel<3, TRANS>), grid, block, 0, s, pa); break;
+    default: hipLaunchKernelGGL((lora_apply_kernel<4, TRANS>), grid, block, 0, s, pa); break;
+  }
+  return launch_status();
+}
+
+// The second half of a pass over activations: expand, or pack and apply.
+template <bool TRANS>
+static moe_status_t launch_out(const LoraExpand& e, uint16_t* pk, hipStream_t s) {
+  return e.out && lora_apply(e.T, e.C) ? launch_apply<TRANS>(e, pk, s) : launch_expand<TRANS>(e, s);
 }
 
 // Rows that a block of the weight gradients sums: an eighth of the batch, at
@@ -594,7 +919,7 @@ static size_t lora_slots(int T) {
 
 static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   const int wide = std::max(p.g[0].out ? p.g[0].C : 0, p.g[1].out ? p.g[1].C : 0);
-  const dim3 grid(p.T / p.chunk + p.NA + 1, (wide + 63) / 64, 2), block(64 * LORA_WAVES);
+  const dim3 grid((wide + 63) / 64, p.T / p.chunk + p.NA + 1, 2), block(64 * LORA_WAVES);
   const moe_status_t st = lora_ranks(p.r, [&](auto N) {
     hipLaunchKernelGGL((lora_wgrad_kernel<decltype(N)::value>), grid, block, 0, s, p);
   });
@@ -605,9 +930,14 @@ static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   return launch_status();
 }
 
+// The packed rank values, at the start of the workspace.
+static size_t lora_pack_bytes(int T, int r) { return (size_t)T * 128 * lora_kh(r); }
+
 static bool lora_sizes_ok(int T, int K, int N, int r, int NA) {
-  return T >= 0 && K > 0 && N > 0 && K % 32 == 0 && N % 32 == 0 && r > 0 && r % 8 == 0 &&
-         NA >= 1 && NA < MOE_MAX_EXPERTS;
+  // (offsets within one adapter's factor are 32-bit; so are positions and tiles)
+  return T >= 0 && T <= (1 << 30) && K > 0 && N > 0 && K % 32 == 0 && N % 32 == 0 &&
+         K <= (1 << 20) && N <= (1 << 20) && r > 0 && r % 8 == 0 && NA >= 1 &&
+         NA < MOE_MAX_EXPERTS;
 }
 
 }  // namespace moe
@@ -618,12 +948,11 @@ extern "C" {
 
 size_t moe_lora_workspace_size(int T, int K, int N, int r, int NA) {
   if (!lora_sizes_ok(T, K, N, r, NA) || T == 0) return 256;
-  const int mt = lora_mt(T, NA);
   // the backward's u, and the partial sums of the reduction with more splits or
   // (once those are used up) of the weight gradients' chunks
-  const int splits = std::max(lora_splits(T, NA, mt, K / 32), lora_splits(T, NA, mt, N / 32));
+  const int splits = std::max(lora_splits(T, NA, K, r), lora_splits(T, NA, N, r));
   const size_t parts = std::max((size_t)splits * T * r, lora_slots(T) * r * ((size_t)K + N));
-  return (((size_t)T * r + parts) * sizeof(float) + 255) / 256 * 256;
+  return lora_pack_bytes(T, r) + (((size_t)T * r + parts) * sizeof(float) + 255) / 256 * 256;
 }
 
 moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* a, void* stream) {
@@ -646,16 +975,18 @@ moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* a, void* stream) {
                                {a->offsets, (size_t)(a->NA + 1) * 4}}) &&
                 outputs_apart({{a->v_out, nt * a->r}, {a->ws, a->ws_bytes}}, {{a->y, ny}}));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int mt = lora_mt(a->T, a->NA), splits = lora_splits(a->T, a->NA, mt, a->K / 32);
-  float* part = static_cast<float*>(a->ws);
+  const int splits = lora_splits(a->T, a->NA, a->K, a->r);
+  uint16_t* pk = static_cast<uint16_t*>(a->ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a->ws) + lora_pack_bytes(a->T, a->r));
   const LoraShrink sh = {static_cast<const uint16_t*>(a->x), static_cast<const uint16_t*>(a->A),
-                         a->offsets, a->src_row, part, a->T, a->K, a->r, a->NA, a->K / 32};
-  moe_status_t st = launch_shrink<false>(sh, mt, splits, s);
+                         a->offsets, a->src_row, part, a->T, a->K, a->r, a->NA,
+                         lora_chunks(a->K, a->r), splits};
+  moe_status_t st = launch_shrink<false>(sh, s);
   if (st != MOE_OK) return st;
   const LoraExpand ex = {part, static_cast<const uint16_t*>(a->B), a->scale, a->offsets, a->src_row,
                          static_cast<const uint16_t*>(a->y), static_cast<uint16_t*>(a->out),
-                         a->v_out, a->T, a->N, a->r, a->NA, splits, 0};
-  return launch_expand<false>(ex, mt, s);
+                         a->v_out, a->T, a->N, a->r, a->NA, splits, 0, 1};
+  return launch_out<false>(ex, pk, s);
 }
 
 moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
@@ -668,7 +999,10 @@ moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
   MOE_CHECK_ARG(a->offsets && (a->dx_out || !a->dx));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const size_t nx = (size_t)a->T * a->K * 2;
-  float* u = static_cast<float*>(a->ws);
+  uint16_t* pk = static_cast<uint16_t*>(a->ws);
+  float* u = a->T > 0 ? reinterpret_cast<float*>(static_cast<char*>(a->ws) +
+                                                 lora_pack_bytes(a->T, a->r))
+                      : nullptr;
   float* part = u + (a->T > 0 ? (size_t)a->T * a->r : 0);
   const bool want_u = a->dx_out || a->dA;
   if (a->T > 0) {
@@ -689,17 +1023,17 @@ moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
                   outputs_apart({{a->dA, 2 * nw * a->K}, {a->dB, 2 * nw * a->N},
                                  {a->ws, a->ws_bytes}}, {{a->dx, nx}}));
     if (want_u) {
-      const int mt = lora_mt(a->T, a->NA), splits = lora_splits(a->T, a->NA, mt, a->N / 32);
+      const int splits = lora_splits(a->T, a->NA, a->N, a->r);
       const LoraShrink sh = {static_cast<const uint16_t*>(a->dy),
                              static_cast<const uint16_t*>(a->B), a->offsets, a->src_row, part,
-                             a->T, a->N, a->r, a->NA, a->N / 32};
-      moe_status_t st = launch_shrink<true>(sh, mt, splits, s);
+                             a->T, a->N, a->r, a->NA, lora_chunks(a->N, a->r), splits};
+      moe_status_t st = launch_shrink<true>(sh, s);
       if (st != MOE_OK) return st;
       const LoraExpand ex = {part, static_cast<const uint16_t*>(a->A), a->scale, a->offsets,
                              a->src_row, static_cast<const uint16_t*>(a->dx),
                              static_cast<uint16_t*>(a->dx_out), a->dA ? u : nullptr, a->T, a->K,
-                             a->r, a->NA, splits, 1};
-      st = launch_expand<true>(ex, mt, s);
+                             a->r, a->NA, splits, 1, 1};
+      st = launch_out<true>(ex, pk, s);
       if (st != MOE_OK) return st;
     }
   }

@@ -153,7 +153,7 @@ def _lora(cls, nb, **kw):
 
 
 SIZE_REFUSALS = (dict(struct_size=8), dict(T=-1), dict(K=0), dict(K=48), dict(N=40), dict(r=0),
-                 dict(r=12), dict(NA=0), dict(NA=1024), dict(dtype=9))
+                 dict(r=12), dict(T=(1 << 30) + 1), dict(K=1 << 21), dict(N=1 << 21), dict(NA=0), dict(NA=1024), dict(dtype=9))
 
 
 def test_lora_refusals(lib):
