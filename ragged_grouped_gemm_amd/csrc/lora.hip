@@ -286,6 +286,48 @@ struct LoraExpand {
   int col_blocks;
 };
 
+// A tile's rank values into LDS: the splits' parts added in order (four loads in
+// flight), scaled and split into two bf16 parts, the high one at the start of a
+// row of `stride` elements and the low one at `lo`, zeros behind either up to
+// `lo` and `len`; rows past the tile are zeros.  The block with `keep` writes v_out.
+__device__ __forceinline__ void stage_ranks(const LoraExpand& p, const LoraTile& tl, int rows,
+                                            bool keep, int lo, int len, uint16_t* vs, int stride) {
+  const float sc = p.scale ? p.scale[tl.a] : 1.0f;
+  const int quads = p.r / 4;
+  for (int i = threadIdx.x; i < rows * quads; i += 64 * LORA_WAVES) {
+    const int row = i / quads, j = (i - row * quads) * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < tl.n) {
+      const float* src = p.part + (size_t)(tl.p0 + row) * p.r + j;
+      const size_t ld = (size_t)p.T * p.r;
+      int k = 0;
+      for (; k + 4 <= p.splits; k += 4) {
+        f32x4 o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const f32x4*>(src + (k + q) * ld);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v += o[q];
+      }
+      for (; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
+      const f32x4 sv = v * sc;
+      if (p.v_out && keep)
+        *reinterpret_cast<f32x4*>(p.v_out + (size_t)(tl.p0 + row) * p.r + j) = p.scale_v ? sv : v;
+      v = sv;
+    }
+    u32x2 hb, lb;
+    split_quad(v, hb, lb);
+    *reinterpret_cast<u32x2*>(vs + row * stride + j) = hb;
+    *reinterpret_cast<u32x2*>(vs + row * stride + lo + j) = lb;
+  }
+  const int gap = (lo - p.r) / 8, pads = (len - 2 * p.r) / 8;
+  const u32x4 zero = {0, 0, 0, 0};
+  for (int i = threadIdx.x; i < rows * pads; i += 64 * LORA_WAVES) {
+    const int row = i / pads, k = i - row * pads;
+    *reinterpret_cast<u32x4*>(vs + row * stride + (k < gap ? p.r + 8 * k : lo + p.r + 8 * (k - gap))) =
+        zero;
+  }
+}
+
 // out[t(p)][c] = y + sum_j s[a] v[p][j] w[a][c][j].  A wave takes chunks of 64
 // columns of the tile's rows, the next chunk's y loaded meanwhile: its four MFMA
 // tiles hold columns 32 (i / 2) + 8 g + 4 (i % 2) + q of lane group g (tile i,
@@ -337,38 +379,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
                        : zero;
   };
   fetch(ch);
-  // the tile's ranks: the splits' parts added in order, four loads in flight
-  const float sc = p.scale ? p.scale[tl.a] : 1.0f;
-  const int quads = p.r / 4;
-  for (int i = threadIdx.x; i < TM * quads; i += 64 * LORA_WAVES) {
-    const int row = i / quads, j = (i - row * quads) * 4;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (row < tl.n) {
-      const float* src = p.part + (size_t)(tl.p0 + row) * p.r + j;
-      const size_t ld = (size_t)p.T * p.r;
-      int k = 0;
-      for (; k + 4 <= p.splits; k += 4) {
-        f32x4 o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const f32x4*>(src + (k + q) * ld);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v += o[q];
-      }
-      for (; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
-      const f32x4 sv = v * sc;
-      if (p.v_out && cb == 0)
-        *reinterpret_cast<f32x4*>(p.v_out + (size_t)(tl.p0 + row) * p.r + j) = p.scale_v ? sv : v;
-      v = sv;
-    }
-    u32x2 hi, lo;
-    split_quad(v, hi, lo);
-    *reinterpret_cast<u32x2*>(&vs[row][j]) = hi;
-    *reinterpret_cast<u32x2*>(&vs[row][p.r + j]) = lo;
-  }
-  // zeros behind the two parts
-  const int tail = (KP - 2 * p.r) / 8;
-  for (int i = threadIdx.x; i < TM * tail; i += 64 * LORA_WAVES)
-    *reinterpret_cast<u32x4*>(&vs[i / tail][2 * p.r + 8 * (i % tail)]) = zero;
+  stage_ranks(p, tl, TM, cb == 0, p.r, KP, &vs[0][0], KP + 8);
   __syncthreads();
   if (!p.out) return;
   const uint16_t* w = p.w + (size_t)tl.a * p.r * p.C;
@@ -436,56 +447,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
   }
 }
 
-// The rank values of all rows between shrink and apply: the splits' parts added
-// in order and split into two bf16 parts, each padded to KH 32-rank steps with
-// zeros: pk[p][hi or lo][32 KH].
-struct LoraPack {
-  const float* part;
-  const float* scale;
-  const int32_t* offsets;
-  uint16_t* pk;
-  float* v_out;
-  int T, r, NA, splits, scale_v, kh;
-};
-
-static constexpr int PACK_ROWS = 32;
-
-__global__ void __launch_bounds__(256) lora_pack_kernel(const LoraPack p) {
-  const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, PACK_ROWS, blockIdx.x);
-  if (tl.n <= 0 || tl.a >= p.NA) return;
-  const float sc = p.scale ? p.scale[tl.a] : 1.0f;
-  const int quads = 8 * p.kh;               // of a padded row
-  for (int i = threadIdx.x; i < tl.n * quads; i += 256) {
-    const int row = i / quads, j = (i - row * quads) * 4;
-    const size_t pos = tl.p0 + row;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j < p.r) {
-      const float* src = p.part + pos * p.r + j;
-      const size_t ld = (size_t)p.T * p.r;
-      for (int k = 0; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
-      const f32x4 sv = v * sc;
-      if (p.v_out) *reinterpret_cast<f32x4*>(p.v_out + pos * p.r + j) = p.scale_v ? sv : v;
-      v = sv;
-    }
-    u32x2 hi, lo;
-    split_quad(v, hi, lo);
-    uint16_t* o = p.pk + pos * (64 * p.kh) + j;
-    *reinterpret_cast<u32x2*>(o) = hi;
-    *reinterpret_cast<u32x2*>(o + 32 * p.kh) = lo;
-  }
-}
-
-struct LoraApply {
-  const uint16_t* pk;
-  const uint16_t* w;          // factor [NA, C, r], or [NA, r, C] (TRANS)
-  const int32_t *offsets, *src_row;
-  const uint16_t* y;          // [T, C] or NULL (zeros)
-  uint16_t* out;              // [T, C], may be y
-  int T, C, r, NA, rows;      // rows of one adapter that a block takes
-  unsigned col_blocks;
-};
-
-static constexpr int APPLY_ROWS = 512;      // at most
+// Rows of one adapter that a block of lora_apply_kernel takes, at most.
+constexpr int apply_rows(int kh) { return kh <= 2 ? 192 : 96; }
 
 // expand for many rows: a wave keeps the factor of its 64 columns in registers
 // and walks its block's rows 16 at a time, the loads of the next DEPTH steps in
@@ -500,17 +463,20 @@ static constexpr int APPLY_ROWS = 512;      // at most
 // nontemporally, and two lanes that hold halves of two rows (l and l ^ 8)
 // swap chunks, so that an instruction covers whole 128-byte lines of 8 rows.
 //
-// The loop over whole steps has no branch and no mask (a step past the last one
-// loads the last one again): behind a load that may not have been issued the
+// The loop over whole steps has no branch and no mask (rows past the last one
+// load the last one again): behind a load that may not have been issued the
 // compiler can only wait for everything, stores included, which emptied the
-// pipeline every round.  Ragged ends, rows without a source and columns past C
-// take a plain loop.
+// pipeline every round.  The last steps, their loads in flight already, are
+// masked; rows without a source and columns past C take a plain loop.
 template <int KH, bool TRANS>
-__global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraApply p) {
+__global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraExpand p,
+                                                                     const int rows) {
   constexpr int DEPTH = KH <= 2 ? 4 : 2;
-  __shared__ int toks[APPLY_ROWS];
+  constexpr int VS = 64 * KH + 8;           // a row's two parts of 32 KH ranks
+  __shared__ int toks[apply_rows(KH)];
+  __shared__ __align__(16) uint16_t vs[apply_rows(KH) * VS];
   const LoraTile tl =
-      lora_tile<false>(p.offsets, p.NA, p.T, p.rows, (int)(blockIdx.x / p.col_blocks));
+      lora_tile<false>(p.offsets, p.NA, p.T, rows, (int)(blockIdx.x / p.col_blocks));
   if (tl.n <= 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & 15, g = lane >> 4;
@@ -528,7 +494,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraA
     return;
   }
   int bad = 0;
-  for (int i = threadIdx.x; i < p.rows; i += 64 * LORA_WAVES) {
+  for (int i = threadIdx.x; i < rows; i += 64 * LORA_WAVES) {
     const int t = i < tl.n ? lora_token(p.src_row, tl.p0 + i, p.T) : -1;
     bad |= i < tl.n && t < 0;
     toks[i] = t;
@@ -551,35 +517,33 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraA
       }
     }
   }
+  stage_ranks(p, tl, (tl.n + 15) & ~15, blockIdx.x % p.col_blocks == 0, 32 * KH, 64 * KH, vs, VS);
   const bool plain = __syncthreads_or(bad) || !p.y || c0 + 64 > p.C;
-  const uint16_t* pk = p.pk + (size_t)tl.p0 * (64 * KH) + 8 * g;
-  auto load_v = [&](int row, u32x4 (&v)[2 * KH]) {
-#pragma unroll
-    for (int k = 0; k < 2 * KH; ++k)
-      v[k] = *reinterpret_cast<const u32x4*>(pk + (size_t)row * (64 * KH) + 32 * k);
-  };
-  auto add = [&](const u32x4 (&v)[2 * KH], const u32x4* y, u32x4* o) {
+  if (c0 >= p.C) return;
+  // o = y + the product, for rows 16 step + l
+  auto add = [&](int step, const u32x4* y, u32x4* o) {
+    const uint16_t* v = vs + (16 * step + l) * VS + 8 * g;
     f32x4 acc[4] = {};
 #pragma unroll
-    for (int k = 0; k < 2 * KH; ++k)
+    for (int k = 0; k < 2 * KH; ++k) {
+      const u32x4 vf = *reinterpret_cast<const u32x4*>(v + 32 * k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = mfma16(wa[k % KH][i], v[k], acc[i]);
+      for (int i = 0; i < 4; ++i) acc[i] = mfma16(wa[k % KH][i], vf, acc[i]);
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) o[q] = add_chunk(y[q], acc[2 * q], acc[2 * q + 1]);
   };
   int s = 0;
-  const int whole = plain ? 0 : tl.n / 16 / DEPTH * DEPTH;
-  if (whole > 0) {
-    u32x4 yr[DEPTH][2], vr[DEPTH][2 * KH];
+  if (!plain) {
+    u32x4 yr[DEPTH][2];
     uint16_t* at[DEPTH][2];
     // instruction q: rows 8 q + (l & 7), chunk 4 (l >> 3) + g of the 128 bytes
     const int col = c0 + 32 * (l >> 3) + 8 * g;
     auto fetch = [&](int d, int step) {
-      const int row = 16 * min(step, whole - 1);
-      load_v(row + l, vr[d]);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const size_t o = (size_t)toks[row + 8 * q + (l & 7)] * p.C + col;
+        const int row = min(16 * step + 8 * q + (l & 7), tl.n - 1);
+        const size_t o = (size_t)toks[row] * p.C + col;
         at[d][q] = p.out + o;
         yr[d][q] = *reinterpret_cast<const u32x4*>(p.y + o);
       }
@@ -600,7 +564,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraA
       for (int d = 0; d < DEPTH; ++d) {
         u32x4 o[2];
         swap(yr[d]);
-        add(vr[d], yr[d], o);
+        add(s + d, yr[d], o);
         swap(o);
         uint16_t* to[2] = {at[d][0], at[d][1]};
         fetch(d, s + DEPTH + d);
@@ -615,12 +579,28 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraA
     // that the loop is entered with the same accesses in flight as it repeats with.
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) fetch(d, d);
-    round();
-    while (s < whole) round();
+    const int whole = tl.n / 16 / DEPTH * DEPTH;
+    if (whole > 0) {
+      round();
+      while (s < whole) round();
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (16 * (s + d) >= tl.n) break;
+      u32x4 o[2];
+      swap(yr[d]);
+      add(s + d, yr[d], o);
+      swap(o);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (16 * (s + d) + 8 * q + (l & 7) < tl.n)
+          __builtin_nontemporal_store(o[q], reinterpret_cast<u32x4*>(at[d][q]));
+    }
+    return;
   }
   for (; 16 * s < tl.n; ++s) {
     const int t = toks[16 * s + l];
-    u32x4 y[2], v[2 * KH], o[2];
+    u32x4 y[2], o[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const u32x4 zero = {0, 0, 0, 0};
@@ -628,8 +608,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraA
                  ? *reinterpret_cast<const u32x4*>(p.y + (size_t)t * p.C + c + 32 * q)
                  : zero;
     }
-    load_v(min(16 * s + l, tl.n - 1), v);
-    add(v, y, o);
+    add(s, y, o);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       if (t >= 0 && c + 32 * q < p.C)
@@ -873,41 +852,32 @@ static moe_status_t launch_expand(LoraExpand p, hipStream_t s) {
   });
 }
 
-// Many rows: pack and apply in place of expand.  They cost a launch more, and
-// pay from about 16 MiB of output on.
-static bool lora_apply(int T, int C) { return (size_t)T * C >= (8u << 20); }
-static int lora_kh(int r) { return (r + 31) / 32; }
-
 template <bool TRANS>
-static moe_status_t launch_apply(const LoraExpand& e, uint16_t* pk, hipStream_t s) {
-  const int kh = lora_kh(e.r);
-  const LoraPack pp = {e.part, e.scale, e.offsets, pk, e.v_out, e.T, e.r, e.NA, e.splits, e.scale_v,
-                       kh};
-  hipLaunchKernelGGL(lora_pack_kernel, dim3(e.T / PACK_ROWS + std::min(e.NA + 1, e.T) + 1), dim3(256),
-                     0, s, pp);
-  moe_status_t st = launch_status();
-  if (st != MOE_OK) return st;
-  const int cols = (e.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
-  // rows a block: about 640 blocks
-  const int rows = std::max(64, std::min(APPLY_ROWS, (int)((size_t)e.T * cols / 640) / 16 * 16));
-  const LoraApply pa = {pk, e.w, e.offsets, e.src_row, e.y, e.out, e.T, e.C, e.r, e.NA, rows,
-                        (unsigned)cols};
-  const size_t blocks = (size_t)(e.T / rows + std::min(e.NA + 1, e.T) + 1) * cols;
+static moe_status_t launch_apply(LoraExpand p, hipStream_t s) {
+  const int kh = (p.r + 31) / 32;
+  const int cols = (p.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
+  // rows a block: about 1300 blocks (measured: 300 to 700 long ones are slower, the
+  // card's many short waits no longer overlap)
+  const int rows = std::max(64, std::min(apply_rows(kh), (int)((size_t)p.T * cols / 1300) / 16 * 16));
+  p.col_blocks = cols;
+  const size_t blocks = (size_t)(p.T / rows + std::min(p.NA + 1, p.T) + 1) * cols;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
   switch (kh) {
-    case 1: hipLaunchKernelGGL((lora_apply_kernel<1, TRANS>), grid, block, 0, s, pa); break;
-    case 2: hipLaunchKernelGGL((lora_apply_kernel<2, TRANS>), grid, block, 0, s, pa); break;
-    case 3: hipLaunchKernelGGL((lora_apply_kernel<3, TRANS>), grid, block, 0, s, pa); break;
-    default: hipLaunchKernelGGL((lora_apply_kernel<4, TRANS>), grid, block, 0, s, pa); break;
+    case 1: hipLaunchKernelGGL((lora_apply_kernel<1, TRANS>), grid, block, 0, s, p, rows); break;
+    case 2: hipLaunchKernelGGL((lora_apply_kernel<2, TRANS>), grid, block, 0, s, p, rows); break;
+    case 3: hipLaunchKernelGGL((lora_apply_kernel<3, TRANS>), grid, block, 0, s, p, rows); break;
+    default: hipLaunchKernelGGL((lora_apply_kernel<4, TRANS>), grid, block, 0, s, p, rows); break;
   }
   return launch_status();
 }
 
-// The second half of a pass over activations: expand, or pack and apply.
+// The second half of a pass over activations: expand, or from 16 MiB of output
+// on (where every adapter has more rows than a row tile) apply.
 template <bool TRANS>
-static moe_status_t launch_out(const LoraExpand& e, uint16_t* pk, hipStream_t s) {
-  return e.out && lora_apply(e.T, e.C) ? launch_apply<TRANS>(e, pk, s) : launch_expand<TRANS>(e, s);
+static moe_status_t launch_out(const LoraExpand& e, hipStream_t s) {
+  const bool many = (size_t)e.T * e.C >= (8u << 20) && e.T >= 64 * e.NA;
+  return e.out && many ? launch_apply<TRANS>(e, s) : launch_expand<TRANS>(e, s);
 }
 
 // Rows that a block of the weight gradients sums: an eighth of the batch, at
@@ -930,9 +900,6 @@ static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   return launch_status();
 }
 
-// The packed rank values, at the start of the workspace.
-static size_t lora_pack_bytes(int T, int r) { return (size_t)T * 128 * lora_kh(r); }
-
 static bool lora_sizes_ok(int T, int K, int N, int r, int NA) {
   // (offsets within one adapter's factor are 32-bit; so are positions and tiles)
   return T >= 0 && T <= (1 << 30) && K > 0 && N > 0 && K % 32 == 0 && N % 32 == 0 &&
@@ -952,7 +919,7 @@ size_t moe_lora_workspace_size(int T, int K, int N, int r, int NA) {
   // (once those are used up) of the weight gradients' chunks
   const int splits = std::max(lora_splits(T, NA, K, r), lora_splits(T, NA, N, r));
   const size_t parts = std::max((size_t)splits * T * r, lora_slots(T) * r * ((size_t)K + N));
-  return lora_pack_bytes(T, r) + (((size_t)T * r + parts) * sizeof(float) + 255) / 256 * 256;
+  return (((size_t)T * r + parts) * sizeof(float) + 255) / 256 * 256;
 }
 
 moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* a, void* stream) {
@@ -976,8 +943,7 @@ moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* a, void* stream) {
                 outputs_apart({{a->v_out, nt * a->r}, {a->ws, a->ws_bytes}}, {{a->y, ny}}));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int splits = lora_splits(a->T, a->NA, a->K, a->r);
-  uint16_t* pk = static_cast<uint16_t*>(a->ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(a->ws) + lora_pack_bytes(a->T, a->r));
+  float* part = static_cast<float*>(a->ws);
   const LoraShrink sh = {static_cast<const uint16_t*>(a->x), static_cast<const uint16_t*>(a->A),
                          a->offsets, a->src_row, part, a->T, a->K, a->r, a->NA,
                          lora_chunks(a->K, a->r), splits};
@@ -986,7 +952,7 @@ moe_status_t moe_lora_fwd(const moe_lora_fwd_args_t* a, void* stream) {
   const LoraExpand ex = {part, static_cast<const uint16_t*>(a->B), a->scale, a->offsets, a->src_row,
                          static_cast<const uint16_t*>(a->y), static_cast<uint16_t*>(a->out),
                          a->v_out, a->T, a->N, a->r, a->NA, splits, 0, 1};
-  return launch_out<false>(ex, pk, s);
+  return launch_out<false>(ex, s);
 }
 
 moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
@@ -999,10 +965,7 @@ moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
   MOE_CHECK_ARG(a->offsets && (a->dx_out || !a->dx));
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const size_t nx = (size_t)a->T * a->K * 2;
-  uint16_t* pk = static_cast<uint16_t*>(a->ws);
-  float* u = a->T > 0 ? reinterpret_cast<float*>(static_cast<char*>(a->ws) +
-                                                 lora_pack_bytes(a->T, a->r))
-                      : nullptr;
+  float* u = static_cast<float*>(a->ws);
   float* part = u + (a->T > 0 ? (size_t)a->T * a->r : 0);
   const bool want_u = a->dx_out || a->dA;
   if (a->T > 0) {
@@ -1033,7 +996,7 @@ moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
                              a->src_row, static_cast<const uint16_t*>(a->dx),
                              static_cast<uint16_t*>(a->dx_out), a->dA ? u : nullptr, a->T, a->K,
                              a->r, a->NA, splits, 1, 1};
-      st = launch_out<true>(ex, pk, s);
+      st = launch_out<true>(ex, s);
       if (st != MOE_OK) return st;
     }
   }
