@@ -779,18 +779,21 @@ __global__ void __launch_bounds__(256) lora_wgrad_sum_kernel(const LoraWgrad p) 
   *o = p.accumulate ? *o + v : v;
 }
 
-// Row tiles of 16, 32 or 64.  A factor's tile is read once per tile of rows, so
-// the highest tile that the adapters fill on average is taken, as long as it
-// leaves `least` tiles.  Shrink, whose tiles are its blocks, asks for 192 (below,
-// it splits the reduction); expand, which has the columns to spread over, for
-// 256 tiles x 256 columns.
-static int lora_mt(int T, int NA, int least) {
-  for (int mt = 4; mt > 1; mt /= 2)
+// Row tiles of 16, 32 or 64 (at most `most` 16s): the highest that the adapters
+// fill on average and that leaves `least` tiles.  A factor's tile is read once
+// per tile of rows, so high tiles save reads of it, while few tiles leave the
+// card empty or cost splits of the reduction.  Shrink, whose tiles are its
+// blocks, asks for 192, above rank 64, where the factor weighs more than the
+// rows, for 96 (8192 rows of rank 128: 41 us with 192, 32 us with 96; of rank
+// 32: 27 and 30 us).  Expand, which has the columns to spread over, asks for
+// 1024 tiles x 256 columns.
+static int lora_mt(int T, int NA, int least, int most) {
+  for (int mt = most; mt > 1; mt /= 2)
     if (T >= 16 * mt * std::max(NA, least)) return mt;
   return 1;
 }
-static int shrink_mt(int T, int NA) { return lora_mt(T, NA, 192); }
-static int expand_mt(int T, int NA, int C) { return lora_mt(T, NA, std::max(1, 256 * 256 / C)); }
+static int shrink_mt(int T, int NA, int r) { return lora_mt(T, NA, r > 64 ? 96 : 192, 4); }
+static int expand_mt(int T, int NA, int C) { return lora_mt(T, NA, std::max(1, 1024 * 256 / C), 2); }
 static int lora_tiles(int T, int NA, int mt) { return T / (16 * mt) + std::min(NA + 1, T) + 1; }
 
 static int lora_rank_tiles(int r) { return r <= 64 ? (r + 15) / 16 : r <= 96 ? 6 : 8; }
@@ -800,9 +803,9 @@ static int lora_chunks(int C, int r) { return lora_rank_tiles(r) <= 4 ? (C + 63)
 // Blocks along a reduction: as many as fill the card, with at least two chunks
 // per wave.
 static int lora_splits(int T, int NA, int C, int r) {
-  const int mt = shrink_mt(T, NA);
+  const int mt = shrink_mt(T, NA, r);
   const int tiles = std::max(1, T / (16 * mt) + (mt == 1 ? std::min(NA, T) / 2 : 0));
-  return std::max(1, std::min({512 / tiles, lora_chunks(C, r) / (2 * LORA_WAVES), 16}));
+  return std::max(1, std::min({(r > 64 ? 320 : 512) / tiles, lora_chunks(C, r) / (2 * LORA_WAVES), 16}));
 }
 
 // Calls f(RT) for the rank tiles that cover r (1, 2, 3, 4, 6 or 8 of 16).
@@ -821,7 +824,7 @@ static moe_status_t lora_ranks(int r, F&& f) {
 
 template <bool TRANS>
 static moe_status_t launch_shrink(const LoraShrink& p, hipStream_t s) {
-  const int mt = shrink_mt(p.T, p.NA);
+  const int mt = shrink_mt(p.T, p.NA, p.r);
   const size_t blocks = (size_t)lora_tiles(p.T, p.NA, mt) * p.splits;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
@@ -837,17 +840,15 @@ template <bool TRANS>
 static moe_status_t launch_expand(LoraExpand p, hipStream_t s) {
   const int mt = expand_mt(p.T, p.NA, p.C);
   // blocks along the columns: one per 256 columns, fewer (each then walks several
-  // chunks and reads the tile's ranks once) as long as the card is filled
-  const int fill = mt == 1 ? 1024 : 512;
+  // chunks and reads the tile's ranks once) as long as 1024 blocks remain
   const int tiles = lora_tiles(p.T, p.NA, mt), cols = (p.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
-  p.col_blocks = p.out ? std::min(cols, std::max(1, fill / tiles)) : 1;
+  p.col_blocks = p.out ? std::min(cols, std::max(1, 1024 / tiles)) : 1;
   const size_t blocks = (size_t)tiles * p.col_blocks;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
   return lora_ranks(p.r, [&](auto N) {
     constexpr int RT = decltype(N)::value;
-    if (mt == 4) hipLaunchKernelGGL((lora_expand_kernel<4, RT, TRANS>), grid, block, 0, s, p);
-    else if (mt == 2) hipLaunchKernelGGL((lora_expand_kernel<2, RT, TRANS>), grid, block, 0, s, p);
+    if (mt == 2) hipLaunchKernelGGL((lora_expand_kernel<2, RT, TRANS>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((lora_expand_kernel<1, RT, TRANS>), grid, block, 0, s, p);
   });
 }
@@ -858,7 +859,7 @@ static moe_status_t launch_apply(LoraExpand p, hipStream_t s) {
   const int cols = (p.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
   // rows a block: about 1300 blocks (measured: 300 to 700 long ones are slower, the
   // card's many short waits no longer overlap)
-  const int rows = std::max(64, std::min(apply_rows(kh), (int)((size_t)p.T * cols / 1300) / 16 * 16));
+  const int rows = std::max(32, std::min(apply_rows(kh), (int)((size_t)p.T * cols / 1300) / 16 * 16));
   p.col_blocks = cols;
   const size_t blocks = (size_t)(p.T / rows + std::min(p.NA + 1, p.T) + 1) * cols;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -872,11 +873,12 @@ static moe_status_t launch_apply(LoraExpand p, hipStream_t s) {
   return launch_status();
 }
 
-// The second half of a pass over activations: expand, or from 16 MiB of output
-// on (where every adapter has more rows than a row tile) apply.
+// The second half of a pass over activations: expand for few rows; apply from 64
+// rows per adapter on, if there are 2 MiB of output (1027 x 5760 at rank 64:
+// 27 us a pass with expand, 22 with apply; 512 x 4096: 11.3 and 10.9).
 template <bool TRANS>
 static moe_status_t launch_out(const LoraExpand& e, hipStream_t s) {
-  const bool many = (size_t)e.T * e.C >= (8u << 20) && e.T >= 64 * e.NA;
+  const bool many = (size_t)e.T * e.C >= (1u << 20) && e.T >= 64 * e.NA;
   return e.out && many ? launch_apply<TRANS>(e, s) : launch_expand<TRANS>(e, s);
 }
 

@@ -112,7 +112,14 @@ struct NormFwd {
   u32x4 *h_out, *x_out, *y_out;
   int T, k, R, chunks;
   float res_scale, eps, inv_d;
+  int stream;               // whether the outputs go past the L2
 };
+
+template <bool STREAM>
+__device__ __forceinline__ void put_chunk(u32x4* p, const u32x4& v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 
 // y[t]'s chunk c from its expert rows, up to four rows' loads in flight (their
 // ids come in one scalar load: one by one they cost 1.5 times the whole kernel).
@@ -151,8 +158,9 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
 }
 
 // Blocks walk the rows; a row's loads are issued while the one before it is
-// reduced, and the channel vectors stay in registers throughout.
-template <class EL, int NC, bool WROW, bool POST, bool PRE, bool COMB>
+// reduced, and the channel vectors stay in registers throughout.  STREAM: h1 and
+// x are stored nontemporally, where they are larger than the L2 anyway.
+template <class EL, int NC, bool WROW, bool POST, bool PRE, bool COMB, bool STREAM>
 __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
   constexpr int V = EL::VEC;
   constexpr bool LOADY = POST && !COMB;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
         for (int q = 0; q < V; ++q) h[i][q] = fmaf(p.res_scale, h[i][q], y[i][q] * (f * wg[i][q]));
-        if (in[i]) p.h_out[row + i * TPR] = store_chunk(h[i], EL());
+        if (in[i]) put_chunk<STREAM>(p.h_out + row + i * TPR, store_chunk(h[i], EL()));
       }
     }
     if constexpr (PRE) {
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
         for (int q = 0; q < V; ++q) h[i][q] *= r * wp[i][q];
-        if (in[i]) p.x_out[row + i * TPR] = store_chunk(h[i], EL());
+        if (in[i]) put_chunk<STREAM>(p.x_out + row + i * TPR, store_chunk(h[i], EL()));
       }
     }
     // a row with only one of the two reductions meets the same LDS half again
@@ -496,8 +504,12 @@ struct LaunchNormFwd {
     const int threads = WROW ? 256 : 64 * waves, rpb = WROW ? 4 : 1;
     const int blocks = std::min((p.T + rpb - 1) / rpb,
                                 device_cu_count() * std::max(1, (COMB ? 960 : 1024) / threads));
-    hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB>), dim3(blocks),
-                       dim3(threads), 0, s, p);
+    if (p.stream)
+      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB, true>), dim3(blocks),
+                         dim3(threads), 0, s, p);
+    else
+      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB, false>),
+                         dim3(blocks), dim3(threads), 0, s, p);
     return launch_status();
   }
   template <int NC, bool WROW>
@@ -567,7 +579,7 @@ moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* a, void* stream
                      a->w_post, a->gate, a->row_gate, a->w_pre, a->row_map, a->topk_w,
                      static_cast<u32x4*>(a->h_out), static_cast<u32x4*>(a->x_out),
                      static_cast<u32x4*>(a->y_out), a->T, k, a->T * k, (int)chunks, a->res_scale,
-                     a->eps, 1.0f / (float)a->d};
+                     a->eps, 1.0f / (float)a->d, n >= (size_t)16 << 20};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const NormGeom g = norm_geom((int)chunks, a->row_map != nullptr);
   return a->dtype == MOE_BF16 ? norm_dispatch(g, LaunchNormFwd<BF16>{p, s})
