@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   constexpr int XS = 64 + 8;
   __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][XS];
   __shared__ float red[LORA_WAVES][16][64 + 4];
-  const LoraGrad& G = p.g[blockIdx.z];
-  const int c0 = blockIdx.x * 64;
+  const LoraGrad& G = p.g[blockIdx.z & 1];
+  const int c0 = blockIdx.x * 64, r0 = (blockIdx.z >> 1) * 16 * RT;
   if (!G.out || c0 >= G.C) return;
   const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.y);
   if (tl.n < 0 || tl.a >= p.NA) return;
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
     for (int j = 0; j < RT; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(16 * j + l, p.r - 1)];
+        uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(r0 + 16 * j + l, p.r - 1)];
     tok = next;
     fetch(tok, x);
     next = tokens(s + 2 * LORA_WAVES);
@@ -719,7 +719,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
         uint32_t b[3][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = 16 * j + l < p.r && (valid >> (8 * g + 2 * q + e) & 1) ? uv[j][2 * q + e] : 0.0f;
+          float v =
+              r0 + 16 * j + l < p.r && (valid >> (8 * g + 2 * q + e) & 1) ? uv[j][2 * q + e] : 0.0f;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             b[k][e] = bf16_of(v);
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
     __syncthreads();
     for (int i = threadIdx.x; i < 16 * 64; i += 64 * LORA_WAVES) {
       const int rr = G.trans ? i % 16 : i / 64, cc = G.trans ? i / 16 : i % 64;
-      const int rank = 16 * j + rr, c = c0 + cc;
+      const int rank = r0 + 16 * j + rr, c = c0 + cc;
       if (rank < p.r && c < G.C) {
         float v = 0.0f;
 #pragma unroll
@@ -891,10 +892,18 @@ static size_t lora_slots(int T) {
 
 static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   const int wide = std::max(p.g[0].out ? p.g[0].C : 0, p.g[1].out ? p.g[1].C : 0);
-  const dim3 grid((wide + 63) / 64, p.T / p.chunk + p.NA + 1, 2), block(64 * LORA_WAVES);
-  const moe_status_t st = lora_ranks(p.r, [&](auto N) {
-    hipLaunchKernelGGL((lora_wgrad_kernel<decltype(N)::value>), grid, block, 0, s, p);
-  });
+  // up to four rank tiles a block: with eight, one wave per SIMD is left, and
+  // nothing covers its waits (2000 rows of rank 128: 58 us against 38)
+  const int tiles = (p.r + 15) / 16, rt = tiles <= 4 ? tiles : tiles <= 6 ? 3 : 4;
+  const dim3 grid((wide + 63) / 64, p.T / p.chunk + p.NA + 1, 2 * ((tiles + rt - 1) / rt));
+  const dim3 block(64 * LORA_WAVES);
+  switch (rt) {
+    case 1: hipLaunchKernelGGL((lora_wgrad_kernel<1>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((lora_wgrad_kernel<2>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((lora_wgrad_kernel<3>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((lora_wgrad_kernel<4>), grid, block, 0, s, p); break;
+  }
+  const moe_status_t st = launch_status();
   if (st != MOE_OK || p.T <= p.chunk) return st;
   const size_t quads = (size_t)p.r * wide / 4;
   hipLaunchKernelGGL(lora_wgrad_sum_kernel, dim3((unsigned)((quads + 255) / 256), p.NA, 2),
