@@ -683,19 +683,19 @@ def _tensor_list(grads, out):
         raise ValueError("all tensors must live on one GPU")
     if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise ValueError("tensors must be contiguous")
-    if out is not None and [t.shape for t in grads] != [t.shape for t in out]:
-        raise ValueError("out must have the shapes of the tensors")
+    numels = list(map(torch.Tensor.numel, grads))
+    if out is not None and numels != list(map(torch.Tensor.numel, out)):
+        raise ValueError("out must have as many elements as the tensors")
     ptrs = list(map(torch.Tensor.data_ptr, tensors))
-    kinds = [t.dtype for t in tensors]
-    bad = set(kinds) - _DT.keys()
-    if bad:
-        raise TypeError(f"unsupported dtype {bad.pop()} (float32 or bfloat16)")
-    kinds = [_DT[k] for k in kinds]
+    try:
+        kinds = [_DT[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]} (float32 or bfloat16)") from None
     # moe_tensor_t is four 8-byte words: data, out, numel, dtype | out_dtype << 32
     words = array.array("q", bytes(32 * n))
     words[0::4] = array.array("q", ptrs[:n])
     words[1::4] = array.array("q", ptrs[-n:])
-    words[2::4] = array.array("q", list(map(torch.Tensor.numel, grads)))
+    words[2::4] = array.array("q", numels)
     words[3::4] = array.array("q", [a | b << 32 for a, b in zip(kinds, kinds[-n:])])
     return (_lib.TensorT * n).from_buffer(words), n, dev
 
@@ -718,7 +718,7 @@ def moe_grad_norm(grads, *, norm=None, ws=None):
 def moe_clip_grad_norm(grads, max_norm, *, out=None, eps=1e-6, norm=None, ws=None):
     """Scale the tensors by min(1, max_norm / (norm + eps)), norm their global
     norm (moe_grad_norm), in place or into ``out`` (one tensor per gradient, of
-    either type).  Returns the norm before clipping, float32 [1]; nothing is
+    as many elements and either type).  Returns the norm before clipping, float32 [1]; nothing is
     read back to the host."""
     arr, n, dev = _tensor_list(grads, out)
     norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm

@@ -81,7 +81,7 @@ def test_clip_in_place(factor):
     _check(gr, keep, ops.moe_clip_grad_norm(gr, max_norm), max_norm)
 
 
-@pytest.mark.parametrize("n", [95, 96, 97, 400])
+@pytest.mark.parametrize("n", [95, 96, 97, 139, 140, 141, 400])
 def test_many_tensors_take_several_launches(n):
     """More tensors than one launch holds; a flat buffer's pieces at odd element offsets."""
     from ragged_grouped_gemm_amd import ops
