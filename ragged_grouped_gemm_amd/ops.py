@@ -535,39 +535,46 @@ def moe_unpermute_combine_bwd(d_out, y, row_map, topk_w, d_y=None, d_topk_w=None
 
 
 def _ptr(t, shape, dtype, dev, name, optional=False):
-    """Address of an argument of the given shape and type on dev (None if optional)."""
+    """Address of an argument of the given shape and type on GPU dev (None if optional)."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    # (one condition: a call checks a dozen tensors, and the host's share is most
+    # of the smallest calls)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must live on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on {_name(dev)}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _name(dev):
+    return "the GPU" if dev < 0 else f"cuda:{dev}"
 
 
 def _call(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.type != "cuda":
+    """fn(*args, stream) on GPU dev's current stream, with dev the current device."""
+    if dev < 0:
         raise ValueError("tensors must live on the GPU")
-    # the raw handle costs 0.1 us, torch.cuda.current_stream() 2.8 us of a 12 us call
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    # the raw handle costs 0.1 us, torch.cuda.current_stream() 2.8 us
+    if dev == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     with torch.cuda.device(dev):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
-def _workspace(ws, nbytes, dev):
-    """(address, bytes) of the caller's workspace, or of a new one (returned to be kept)."""
+def _workspace(ws, nbytes, like):
+    """(workspace, its address, its bytes): the caller's, or a new one of nbytes()
+    (the library refuses one that is too small)."""
     if ws is None:
-        ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous and live on {dev}")
+        ws = torch.empty((max(nbytes(), 1),), dtype=torch.uint8, device=like.device)
+    elif ws.get_device() != like.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and live on {like.device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -588,7 +595,7 @@ def moe_block_norm_fwd(h, y=None, *, w_post=None, gate=None, row_gate=None, res_
     if h.dim() != 2:
         raise ValueError("h must be [T, d]")
     T, d = h.shape
-    dt, dev, f32 = h.dtype, h.device, torch.float32
+    dt, dev, f32 = h.dtype, h.get_device(), torch.float32
     k = 0
     if row_map is not None:
         k = row_map.shape[-1]
@@ -638,11 +645,11 @@ def moe_block_norm_bwd(h1, y=None, *, dh1=None, dx=None, w_post=None, gate=None,
     if ref is None or ref.dim() != 2:
         raise ValueError("h1 (or y) must be [T, d]")
     T, d = ref.shape
-    dt, dev, f32 = ref.dtype, ref.device, torch.float32
+    dt, dev, f32 = ref.dtype, ref.get_device(), torch.float32
     if accumulate and any(w is not None and g is None for w, g in
                           ((w_post, dw_post), (gate, dgate), (w_pre, dw_pre))):
         raise ValueError("accumulate needs the gradients to add to")
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=ref.device)
     dh = new((T, d), dt) if dh is None else dh
     if y is not None and dy is None:
         dy = new((T, d), dt)
@@ -654,7 +661,7 @@ def moe_block_norm_bwd(h1, y=None, *, dh1=None, dx=None, w_post=None, gate=None,
         drow_gate = new((T,), f32)
     if w_pre is not None and dw_pre is None:
         dw_pre = new((d,), f32)
-    ws, wp, wb = _workspace(ws, moe_block_norm_bwd_workspace_size(T, d), dev)
+    ws, wp, wb = _workspace(ws, lambda: moe_block_norm_bwd_workspace_size(T, d), ref)
     args = _lib.BlockNormBwdArgs(
         ctypes.sizeof(_lib.BlockNormBwdArgs), _dtype(ref), T, d, res_scale, eps, int(accumulate),
         _ptr(h1, (T, d), dt, dev, "h1", True), _ptr(y, (T, d), dt, dev, "y", True),
@@ -676,7 +683,7 @@ def _tensor_list(grads, out):
         raise ValueError("an empty list of tensors")
     if out is not None and len(out) != n:
         raise ValueError(f"{len(out)} outputs for {n} tensors")
-    dev = grads[0].device
+    dev = grads[0].get_device()
     # attribute by attribute: a list of each costs less than a loop body per tensor
     tensors = grads if out is None else [*grads, *out]
     if len(set(map(torch.Tensor.get_device, tensors))) != 1:
@@ -708,8 +715,8 @@ def moe_grad_norm(grads, *, norm=None, ws=None):
     """sqrt of the sum of squares of all elements of the tensors (float32 or
     bfloat16, summed in float64), as a float32 tensor [1] on their device."""
     arr, n, dev = _tensor_list(grads, None)
-    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
-    ws, wp, wb = _workspace(ws, moe_grad_norm_workspace_size(n), dev)
+    norm = _empty((1,), torch.float32, grads[0]) if norm is None else norm
+    ws, wp, wb = _workspace(ws, lambda: moe_grad_norm_workspace_size(n), grads[0])
     check(_call(dev, _lib.load().moe_grad_norm, arr, n, _ptr(norm, (1,), torch.float32, dev, "norm"),
                 wp, wb), "moe_grad_norm")
     return norm
@@ -721,8 +728,8 @@ def moe_clip_grad_norm(grads, max_norm, *, out=None, eps=1e-6, norm=None, ws=Non
     as many elements and either type).  Returns the norm before clipping, float32 [1]; nothing is
     read back to the host."""
     arr, n, dev = _tensor_list(grads, out)
-    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
-    ws, wp, wb = _workspace(ws, moe_grad_norm_workspace_size(n), dev)
+    norm = _empty((1,), torch.float32, grads[0]) if norm is None else norm
+    ws, wp, wb = _workspace(ws, lambda: moe_grad_norm_workspace_size(n), grads[0])
     check(_call(dev, _lib.load().moe_clip_grad_norm, arr, n, max_norm, eps,
                 _ptr(norm, (1,), torch.float32, dev, "norm"), wp, wb), "moe_clip_grad_norm")
     return norm
@@ -752,11 +759,11 @@ def moe_lora_fwd(x, A, B, offsets, y, *, src_row=None, scale=None, out=None, v_o
     Returns (out, v or None); v = x A^T [T, r] float32, by position, with v_out
     or want_v (for moe_lora_bwd)."""
     T, K, N, r, NA = _lora_sizes(x, A, B, offsets)
-    bf, f32, dev = x.dtype, torch.float32, x.device
+    bf, f32, dev = x.dtype, torch.float32, x.get_device()
     out = y if out is None else out
     if want_v and v_out is None:
-        v_out = torch.zeros((T, r), dtype=f32, device=dev)
-    ws, wp, wb = _workspace(ws, moe_lora_workspace_size(T, K, N, r, NA), dev)
+        v_out = torch.zeros((T, r), dtype=f32, device=x.device)
+    ws, wp, wb = _workspace(ws, lambda: moe_lora_workspace_size(T, K, N, r, NA), x)
     args = _lib.LoraFwdArgs(
         ctypes.sizeof(_lib.LoraFwdArgs), _dtype(x), T, K, N, r, NA, _ptr(x, (T, K), bf, dev, "x"),
         _ptr(A, (NA, r, K), bf, dev, "A"), _ptr(B, (NA, N, r), bf, dev, "B"),
@@ -775,15 +782,15 @@ def moe_lora_bwd(x, dy, A, B, offsets, v, *, src_row=None, scale=None, dx=None, 
     dx_out None: dx in place, or a new tensor), dA[a] = u^T x and
     dB[a] = scale[a] dy^T v, float32, v the forward's.  Returns (dx_out, dA, dB)."""
     T, K, N, r, NA = _lora_sizes(x, A, B, offsets)
-    bf, f32, dev = x.dtype, torch.float32, x.device
+    bf, f32, dev = x.dtype, torch.float32, x.get_device()
     if accumulate and want_dw and (dA is None or dB is None):
         raise ValueError("accumulate needs the gradients to add to")
     if want_dx and dx_out is None:
         dx_out = torch.empty_like(x) if dx is None else dx
     if want_dw:
-        dA = torch.empty(A.shape, dtype=f32, device=dev) if dA is None else dA
-        dB = torch.empty(B.shape, dtype=f32, device=dev) if dB is None else dB
-    ws, wp, wb = _workspace(ws, moe_lora_workspace_size(T, K, N, r, NA), dev)
+        dA = _empty(A.shape, f32, x) if dA is None else dA
+        dB = _empty(B.shape, f32, x) if dB is None else dB
+    ws, wp, wb = _workspace(ws, lambda: moe_lora_workspace_size(T, K, N, r, NA), x)
     args = _lib.LoraBwdArgs(
         ctypes.sizeof(_lib.LoraBwdArgs), _dtype(x), T, K, N, r, NA, int(accumulate),
         _ptr(x, (T, K), bf, dev, "x"), _ptr(dy, (T, N), bf, dev, "dy"),
