@@ -33,28 +33,32 @@
 
 namespace moe {
 
-// A row belongs to one wave (WROW: rows of up to 64 NC chunks, several to a
-// block) or to a whole block of ceil(chunks / (64 NC)) waves.  A lane owns the
-// 16-byte chunks lt, lt + tpr, ... of its row (NC of them; tpr lanes a row), so
-// only the last wave of a row can have idle lanes.
-template <bool WROW>
+// A row belongs to LPR lanes of a wave (8, 16, 32 or all 64: rows of up to LPR NC
+// chunks, several to a block), or (LPR 0) to a whole block of
+// ceil(chunks / (64 NC)) waves.  A lane owns the 16-byte chunks lt, lt + tpr, ...
+// of its row (NC of them; tpr lanes a row).
+template <int LPR>
 struct NormPlace {
   int tpr, lt, sub;      // lanes per row; lane within the row; row within the block
   __device__ __forceinline__ NormPlace()
-      : tpr(WROW ? 64 : blockDim.x),
-        lt(WROW ? threadIdx.x & 63 : threadIdx.x),
-        sub(WROW ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0) {}
+      : tpr(LPR ? LPR : blockDim.x),
+        lt(LPR ? threadIdx.x & (LPR - 1) : threadIdx.x),
+        sub(LPR == 64  ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+            : LPR > 0 ? threadIdx.x / (LPR > 0 ? LPR : 1)
+                      : 0) {}
 };
 
 // Sums of NV <= 4 values over a row's lanes, on every lane.  A wave's
 // butterfly, then one over the row's waves through LDS.  `half` alternates
 // between two halves: a thread writes one half again only after the barrier
 // of the other, which every thread reaches after reading the first.
-template <int NV, bool WROW>
+template <int NV, int LPR>
 __device__ __forceinline__ void row_sums(float (&v)[NV], f32x4 (*lds)[16], int half) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (!WROW) {
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int o = (LPR ? LPR : 64) / 2; o >= 1; o >>= 1) v[i] += __shfl_xor(v[i], o, 64);
+  if constexpr (LPR == 0) {
     f32x4* b = lds[half];
     if ((threadIdx.x & 63) == 0) {
       f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -160,13 +164,13 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
 // Blocks walk the rows; a row's loads are issued while the one before it is
 // reduced, and the channel vectors stay in registers throughout.  STREAM: h1 and
 // x are stored nontemporally, where they are larger than the L2 anyway.
-template <class EL, int NC, bool WROW, bool POST, bool PRE, bool COMB, bool STREAM>
-__global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
+template <class EL, int NC, int LPR, bool POST, bool PRE, bool COMB, bool STREAM>
+__global__ void __launch_bounds__(LPR ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
   constexpr int V = EL::VEC;
   constexpr bool LOADY = POST && !COMB;
   __shared__ f32x4 lds[2][16];
-  const NormPlace<WROW> pl;
-  const int lt = pl.lt, TPR = pl.tpr, rpb = WROW ? blockDim.x >> 6 : 1;
+  const NormPlace<LPR> pl;
+  const int lt = pl.lt, TPR = pl.tpr, rpb = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
   int t = blockIdx.x * rpb + pl.sub;
   const int step = gridDim.x * rpb;
   bool in[NC];
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const
       }
       float f = p.row_gate ? p.row_gate[t] : 1.0f;
       if (p.w_post) {
-        row_sums<1, WROW>(s, lds, 0);
+        row_sums<1, LPR>(s, lds, 0);
         f *= 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
       }
 #pragma unroll
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int q = 0; q < V; ++q) s[0] = fmaf(h[i][q], h[i][q], s[0]);
-      row_sums<1, WROW>(s, lds, 1);
+      row_sums<1, LPR>(s, lds, 1);
       const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -254,8 +258,13 @@ __global__ void __launch_bounds__(WROW ? 256 : 1024) block_norm_fwd_kernel(const
     }
     // a row with only one of the two reductions meets the same LDS half again
     // in the next step
-    if (!WROW && !(PRE && POST && p.w_post)) __syncthreads();
+    if (LPR == 0 && !(PRE && POST && p.w_post)) __syncthreads();
   }
+}
+
+// Threads of a block of the backward.
+constexpr int norm_bwd_threads(int nc, int lpr, int waves) {
+  return lpr == 0 ? 64 * waves : lpr == 64 ? (nc == 1 ? 1024 : 512) : 256;
 }
 
 struct NormBwd {
@@ -268,13 +277,13 @@ struct NormBwd {
   float res_scale, eps, inv_d;
 };
 
-template <class EL, int NC, bool WROW, bool POST, bool PRE>
-__global__ void __launch_bounds__(WROW && NC > 1 ? 512 : 1024) block_norm_bwd_kernel(
+template <class EL, int NC, int LPR, bool POST, bool PRE>
+__global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_kernel(
     const NormBwd p) {
   constexpr int V = EL::VEC;
   __shared__ f32x4 lds[2][16];
-  const NormPlace<WROW> pl;
-  const int lt = pl.lt, TPR = pl.tpr, rpb = WROW ? blockDim.x >> 6 : 1;
+  const NormPlace<LPR> pl;
+  const int lt = pl.lt, TPR = pl.tpr, rpb = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
   const int step = gridDim.x * rpb;
   bool in[NC];
 #pragma unroll
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(WROW && NC > 1 ? 512 : 1024) block_norm_bwd_ke
         }
         if constexpr (POST) s[2] = fmaf(y[i][q], y[i][q], s[2]);
       }
-    if (PRE || p.w_post) row_sums<3, WROW>(s, lds, 0);
+    if (PRE || p.w_post) row_sums<3, LPR>(s, lds, 0);
     if constexpr (PRE) {
       const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
       const float m = -r * r * (s[1] * p.inv_d);
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(WROW && NC > 1 ? 512 : 1024) block_norm_bwd_ke
           D[i][q] *= wg[i][q];
           s2[0] = fmaf(D[i][q], y[i][q], s2[0]);
         }
-      if (p.w_post || p.drow_gate) row_sums<1, WROW>(s2, lds, 1);
+      if (p.w_post || p.drow_gate) row_sums<1, LPR>(s2, lds, 1);
       if (p.drow_gate && lt == 0) p.drow_gate[t] = ry * s2[0];
       const float m = p.w_post ? -f * (ry * ry * (s2[0] * p.inv_d)) : 0.0f;
 #pragma unroll
@@ -381,22 +390,29 @@ __global__ void __launch_bounds__(WROW && NC > 1 ? 512 : 1024) block_norm_bwd_ke
       }
     }
     // a row with only one of the two reductions meets the same LDS half again
-    if (!WROW && !(POST && p.w_post)) __syncthreads();
+    if (LPR == 0 && !(POST && p.w_post)) __syncthreads();
   }
-  // one row of sums per block: the rows of a block (one a wave) are added in order
+  // one row of sums per block: a wave's rows are added in a butterfly, the waves
+  // of a block that holds several rows in order
   auto put = [&](float* part, float (&a)[NC][V]) {
     if (!part) return;
     float* o = part + (size_t)blockIdx.x * p.chunks * V;
-    if constexpr (WROW) {
-      __shared__ float acc[NC * 64 * V];
-      for (int w = 0; w < rpb; ++w) {
+    if constexpr (LPR > 0) {
+      __shared__ __align__(16) float acc[NC * LPR * V];
+#pragma unroll
+      for (int m = LPR; m < 64; m <<= 1)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int q = 0; q < V; ++q) a[i][q] += __shfl_xor(a[i][q], m, 64);
+      for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
         __syncthreads();
-        if (w != pl.sub) continue;
+        if (w != (int)(threadIdx.x >> 6) || (threadIdx.x & 63) >= LPR) continue;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int q = 0; q < V; q += 4) {
-            float* s = acc + (lt + i * 64) * V + q;
+            float* s = acc + (lt + i * LPR) * V + q;
             f32x4 v = {a[i][q], a[i][q + 1], a[i][q + 2], a[i][q + 3]};
             if (w) v = *reinterpret_cast<f32x4*>(s) + v;
             *reinterpret_cast<f32x4*>(s) = v;
@@ -461,24 +477,33 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const NormFinis
   }
 }
 
-// The geometry of a row: chunks per lane, and waves per row (0: a wave a row).
+// The geometry of a row: chunks per lane, lanes of a wave per row (0: the row has
+// a block), waves per row of a block.
 struct NormGeom {
-  int nc, waves;
+  int nc, lpr, waves;
 };
 static NormGeom norm_geom(int chunks, bool comb = false) {
-  if (chunks <= 64) return {1, 0};
-  if (chunks <= 128) return {2, 0};
+  if (chunks <= 8) return {1, 8, 0};
+  if (chunks <= 16) return {1, 16, 0};
+  if (chunks <= 32) return {1, 32, 0};
+  if (chunks <= 64) return {1, 64, 0};
+  if (chunks <= 128) return {2, 64, 0};
   const int nc = chunks <= 1024 && !comb ? 1 : chunks <= 2048 ? 2 : 4;
-  return {nc, (chunks + 64 * nc - 1) / (64 * nc)};
+  return {nc, 0, (chunks + 64 * nc - 1) / (64 * nc)};
 }
 
-// Calls f.template run<NC, WROW>(waves per row) for a row of `chunks` chunks.
+// Calls f.template run<NC, LPR>(waves per row) for a row's geometry.
 template <class F>
 static moe_status_t norm_dispatch(const NormGeom& g, F&& f) {
-  if (!g.waves) return g.nc == 1 ? f.template run<1, true>(0) : f.template run<2, true>(0);
-  return g.nc == 1   ? f.template run<1, false>(g.waves)
-         : g.nc == 2 ? f.template run<2, false>(g.waves)
-                     : f.template run<4, false>(g.waves);
+  switch (g.lpr) {
+    case 8: return f.template run<1, 8>(0);
+    case 16: return f.template run<1, 16>(0);
+    case 32: return f.template run<1, 32>(0);
+    case 64: return g.nc == 1 ? f.template run<1, 64>(0) : f.template run<2, 64>(0);
+  }
+  return g.nc == 1   ? f.template run<1, 0>(g.waves)
+         : g.nc == 2 ? f.template run<2, 0>(g.waves)
+                     : f.template run<4, 0>(g.waves);
 }
 
 static constexpr int NORM_MAX_CHUNKS = 4096;
@@ -490,8 +515,8 @@ static constexpr int NORM_MAX_ROWS = INT32_MAX - (1 << 20);
 // channel sums is the same everywhere.
 static int norm_bwd_blocks(int T, int chunks) {
   const NormGeom g = norm_geom(chunks);
-  const int rpb = g.waves ? 1 : g.nc == 1 ? 16 : 8;
-  const int per_cu = g.waves ? std::max(1, std::min(4, 16 / g.waves)) : 1;
+  const int threads = norm_bwd_threads(g.nc, g.lpr, g.waves), rpb = g.lpr ? threads / g.lpr : 1;
+  const int per_cu = g.lpr == 64 ? 1 : std::max(1, std::min(4, 1024 / threads));
   return std::min((T + rpb - 1) / rpb, 256 * per_cu);
 }
 
@@ -499,25 +524,25 @@ template <class EL>
 struct LaunchNormFwd {
   const NormFwd& p;
   hipStream_t s;
-  template <int NC, bool WROW, bool POST, bool PRE, bool COMB>
+  template <int NC, int LPR, bool POST, bool PRE, bool COMB>
   moe_status_t go(int waves) const {
-    const int threads = WROW ? 256 : 64 * waves, rpb = WROW ? 4 : 1;
+    const int threads = LPR ? 256 : 64 * waves, rpb = LPR ? threads / (LPR ? LPR : 1) : 1;
     const int blocks = std::min((p.T + rpb - 1) / rpb,
                                 device_cu_count() * std::max(1, (COMB ? 960 : 1024) / threads));
     if (p.stream)
-      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB, true>), dim3(blocks),
+      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, LPR, POST, PRE, COMB, true>), dim3(blocks),
                          dim3(threads), 0, s, p);
     else
-      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, WROW, POST, PRE, COMB, false>),
+      hipLaunchKernelGGL((block_norm_fwd_kernel<EL, NC, LPR, POST, PRE, COMB, false>),
                          dim3(blocks), dim3(threads), 0, s, p);
     return launch_status();
   }
-  template <int NC, bool WROW>
+  template <int NC, int LPR>
   moe_status_t run(int waves) const {
-    if (!p.y) return go<NC, WROW, false, true, false>(waves);
+    if (!p.y) return go<NC, LPR, false, true, false>(waves);
     if (p.row_map)
-      return p.x_out ? go<NC, WROW, true, true, true>(waves) : go<NC, WROW, true, false, true>(waves);
-    return p.x_out ? go<NC, WROW, true, true, false>(waves) : go<NC, WROW, true, false, false>(waves);
+      return p.x_out ? go<NC, LPR, true, true, true>(waves) : go<NC, LPR, true, false, true>(waves);
+    return p.x_out ? go<NC, LPR, true, true, false>(waves) : go<NC, LPR, true, false, false>(waves);
   }
 };
 
@@ -526,17 +551,17 @@ struct LaunchNormBwd {
   const NormBwd& p;
   hipStream_t s;
   int blocks;
-  template <int NC, bool WROW, bool POST, bool PRE>
+  template <int NC, int LPR, bool POST, bool PRE>
   moe_status_t go(int waves) const {
-    const int threads = WROW ? (NC == 1 ? 1024 : 512) : 64 * waves;
-    hipLaunchKernelGGL((block_norm_bwd_kernel<EL, NC, WROW, POST, PRE>), dim3(blocks),
+    const int threads = norm_bwd_threads(NC, LPR, waves);
+    hipLaunchKernelGGL((block_norm_bwd_kernel<EL, NC, LPR, POST, PRE>), dim3(blocks),
                        dim3(threads), 0, s, p);
     return launch_status();
   }
-  template <int NC, bool WROW>
+  template <int NC, int LPR>
   moe_status_t run(int waves) const {
-    if (!p.y) return go<NC, WROW, false, true>(waves);
-    return p.dx ? go<NC, WROW, true, true>(waves) : go<NC, WROW, true, false>(waves);
+    if (!p.y) return go<NC, LPR, false, true>(waves);
+    return p.dx ? go<NC, LPR, true, true>(waves) : go<NC, LPR, true, false>(waves);
   }
 };
 

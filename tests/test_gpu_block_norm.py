@@ -89,7 +89,8 @@ class Case:
 
 # widths: one chunk, a wave's row with a partial chunk, each geometry's start and
 # end, the widest rows
-WIDTHS = [("bf16", 8), ("bf16", 504), ("bf16", 512), ("bf16", 520), ("bf16", 1024), ("bf16", 2048),
+WIDTHS = [("bf16", 8), ("bf16", 64), ("bf16", 72), ("bf16", 128), ("bf16", 200), ("bf16", 256),
+          ("bf16", 264), ("f32", 32), ("f32", 36), ("f32", 100), ("bf16", 504), ("bf16", 512), ("bf16", 520), ("bf16", 1024), ("bf16", 2048),
           ("bf16", 2880), ("bf16", 4104), ("bf16", 7168), ("bf16", 8200), ("bf16", 16384),
           ("bf16", 32768), ("f32", 4), ("f32", 260), ("f32", 1000), ("f32", 2880), ("f32", 7168),
           ("f32", 16384)]
@@ -113,7 +114,8 @@ def test_backward_widths(dtype, d):
 
 
 @pytest.mark.parametrize("flags", FLAGS)
-@pytest.mark.parametrize("dtype,T,d", [("bf16", 1, 2880), ("bf16", 131, 512), ("f32", 67, 1032)])
+@pytest.mark.parametrize("dtype,T,d", [("bf16", 1, 2880), ("bf16", 131, 512), ("f32", 67, 1032),
+                                       ("bf16", 77, 40), ("f32", 39, 60), ("bf16", 45, 248)])
 def test_every_combination_of_stages(dtype, T, d, flags):
     note(f"block_norm {dtype} T={T} d={d} {flags}")
     c = Case(T, d, dtype, flags)
@@ -123,8 +125,9 @@ def test_every_combination_of_stages(dtype, T, d, flags):
     c.check_backward(c.backward())
 
 
-@pytest.mark.parametrize("T", [1, 511, 512, 513, 2500])
-@pytest.mark.parametrize("dtype,d", [("bf16", 256), ("bf16", 2048), ("f32", 1024)])
+@pytest.mark.parametrize("T", [1, 511, 512, 513, 2500, 40000])
+@pytest.mark.parametrize("dtype,d", [("bf16", 256), ("bf16", 2048), ("f32", 1024), ("bf16", 56),
+                                     ("f32", 16)])
 def test_many_rows(dtype, d, T):
     """Row counts around the backward's row groups; the same call twice gives the same bits."""
     note(f"block_norm rows {dtype} T={T} d={d}")
@@ -138,7 +141,8 @@ def test_many_rows(dtype, d, T):
 
 
 @pytest.mark.parametrize("k", [1, 2, 3, 4, 6, 8, 32])
-@pytest.mark.parametrize("dtype,T,d", [("bf16", 37, 2880), ("f32", 50, 128), ("bf16", 9, 7168)])
+@pytest.mark.parametrize("dtype,T,d", [("bf16", 37, 2880), ("f32", 50, 128), ("bf16", 9, 7168),
+                                       ("bf16", 33, 64)])
 def test_combine_fused(dtype, T, d, k):
     """y combined from expert rows; the kept y is the combine's own result."""
     from ragged_grouped_gemm_amd import ops
