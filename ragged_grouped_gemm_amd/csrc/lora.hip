@@ -13,11 +13,17 @@
 // Two kernels make a pass over activations: `shrink` reduces a tile of rows to
 // its r values (the reduction split over waves, and over blocks where there are
 // few rows; a block's partial sums go to the workspace and are added in order),
-// `expand` adds their products with the other factor to the wide rows.  The r
-// values stay float32 between the two: in front of the bf16 matrix cores each
-// is split into a high and a low bf16 part (x = hi + lo up to 2^-17 |x|), laid
-// side by side along the reduction, so a step over 32 covers 16 ranks at
-// twice bf16's precision.  Weight gradients are float32 throughout.
+// and `expand` (few rows) or `apply` (many) adds their products with the other
+// factor to the wide rows.  The r values stay float32 between the two: in front
+// of the bf16 matrix cores each is split into a high and a low bf16 part, which
+// leave out at most 2^-16 of it (a float32 matrix instruction would run at a
+// sixteenth of the rate).  Weight gradients are float32 throughout.
+//
+// Measured, as whole calls: 64 rows of 32 adapters, rank 16, 7168 x 7168: 11 us
+// (two launches, each at the 5 us that its chain of dependent loads takes);
+// 8192 rows of 16 adapters, rank 32, 7168 x 4096: 57 us, 4.4 TB/s of what must
+// be moved; backward of 8192 rows of 8 adapters, rank 16, 4096 x 4096: 78 us,
+// 3.4 TB/s.  A large copy on the same card reaches 4.9 TB/s.
 #include "common.hpp"
 #include "spans.hpp"
 
@@ -144,9 +150,11 @@ struct LoraShrink {
 // part[split][p][j] = sum over the split's share of C of x[t(p)][c] w[a][j][c].
 // The waves share the block's chunks of KC columns.  A wave stages its chunk of
 // the rows and of the factor through LDS of its own: whole lines are loaded
-// (KC / 8 lanes a row) while the chunk before is multiplied; loading MFMA
-// fragments straight from memory, 16 bytes from each of 16 rows at a time, kept
-// the address units busier than the memory.  MFMA: first operand the factor's
+// (KC / 8 lanes a row) while the chunk before is multiplied.  8192 x 7168 rows of
+// rank 32: 27 us (3.9 TB/s; 36 us with MFMA fragments loaded straight from
+// memory, 16 bytes from each of 16 rows at a time); what is left over the copy
+// rate is the start of the blocks, three loads deep (offsets, source rows,
+// rows), and their end.  MFMA: first operand the factor's
 // rows (register 4 (lane >> 4) + q = rank), second the activation rows
 // (lane & 15).  A factor whose reduction runs over its rows (TRANS) is read
 // transposed.
@@ -332,8 +340,8 @@ __device__ __forceinline__ void stage_ranks(const LoraExpand& p, const LoraTile&
 // columns of the tile's rows, the next chunk's y loaded meanwhile: its four MFMA
 // tiles hold columns 32 (i / 2) + 8 g + 4 (i % 2) + q of lane group g (tile i,
 // register q), so a lane ends up with two runs of 8 columns of its row and each
-// load of y and store of out covers 64 contiguous bytes of 16 rows.  A factor stored the other way
-// (TRANS) passes through LDS and is read transposed.
+// load of y and store of out covers 64 contiguous bytes of 16 rows.  A factor
+// stored the other way (TRANS) passes through LDS and is read transposed.
 template <int MT, int RT, bool TRANS>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const LoraExpand p) {
   constexpr int TM = 16 * MT, R = 16 * RT;
@@ -462,6 +470,8 @@ constexpr int apply_rows(int kh) { return kh <= 2 ? 192 : 96; }
 // come first in the grid, the outputs (far larger than the L2) are stored
 // nontemporally, and two lanes that hold halves of two rows (l and l ^ 8)
 // swap chunks, so that an instruction covers whole 128-byte lines of 8 rows.
+// 8192 x 4096 at rank 32: 37 us, of which the rows' loop takes half; the blocks
+// start together, and their first loads (factor, rank values, rows) queue up.
 //
 // The loop over whole steps has no branch and no mask (rows past the last one
 // load the last one again): behind a load that may not have been issued the
@@ -785,7 +795,7 @@ __global__ void __launch_bounds__(256) lora_wgrad_sum_kernel(const LoraWgrad p) 
 // per tile of rows, so high tiles save reads of it, while few tiles leave the
 // card empty or cost splits of the reduction.  Shrink, whose tiles are its
 // blocks, asks for 192, above rank 64, where the factor weighs more than the
-// rows, for 96 (8192 rows of rank 128: 41 us with 192, 32 us with 96; of rank
+// rows, for 96 (8192 rows of rank 128: 41 us with 192, 38 us with 96; of rank
 // 32: 27 and 30 us).  Expand, which has the columns to spread over, asks for
 // 1024 tiles x 256 columns.
 static int lora_mt(int T, int NA, int least, int most) {
@@ -860,7 +870,8 @@ static moe_status_t launch_apply(LoraExpand p, hipStream_t s) {
   const int cols = (p.C + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
   // rows a block: about 1300 blocks (measured: 300 to 700 long ones are slower, the
   // card's many short waits no longer overlap)
-  const int rows = std::max(32, std::min(apply_rows(kh), (int)((size_t)p.T * cols / 1300) / 16 * 16));
+  const size_t share = (size_t)p.T * cols / 1300 / 16 * 16;
+  const int rows = std::max(32, (int)std::min((size_t)apply_rows(kh), share));
   p.col_blocks = cols;
   const size_t blocks = (size_t)(p.T / rows + std::min(p.NA + 1, p.T) + 1) * cols;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;

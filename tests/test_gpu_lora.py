@@ -103,10 +103,15 @@ CASES = [(1, 64, 32, 8, 1), (1, 7168, 7168, 16, 32), (7, 96, 160, 24, 3), (64, 2
          (300, 160, 128, 96, 1), (260, 128, 64, 112, 4), (40, 64, 64, 8, 1022),
          (2048, 512, 512, 16, 1),
          # row tiles of 64; gradients over several chunks of 1024 rows, and one adapter of most rows
-         (6200, 96, 160, 16, 2), (9000, 64, 96, 24, 3), (2300, 128, 64, 128, 2)]
+         (6200, 96, 160, 16, 2), (9000, 64, 96, 24, 3), (2300, 128, 64, 128, 2),
+         # the kernel for many rows at each of its rank steps, columns past whole 64s
+         (4200, 288, 256, 16, 3), (4200, 256, 288, 40, 2), (4100, 352, 320, 88, 1),
+         (4300, 288, 288, 120, 3)]
+# row tiles of 64 in the reduction, at every rank tile count (few columns: the oracle is dense)
+TALL = [(12400, 64, 96, r, 2) for r in (8, 32, 48, 64)] + [(6300, 96, 64, r, 3) for r in (72, 104)]
 
 
-@pytest.mark.parametrize("T,K,N,r,NA", CASES)
+@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL)
 def test_forward(T, K, N, r, NA):
     note(f"lora_fwd T={T} K={K} N={N} r={r} NA={NA}")
     c = Case(T, K, N, r, NA)
@@ -119,7 +124,7 @@ def test_forward(T, K, N, r, NA):
     assert none is None and inplace is c.y[1] and torch.equal(inplace, out)
 
 
-@pytest.mark.parametrize("T,K,N,r,NA", CASES)
+@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL)
 def test_backward(T, K, N, r, NA):
     note(f"lora_bwd T={T} K={K} N={N} r={r} NA={NA}")
     c = Case(T, K, N, r, NA)
