@@ -294,8 +294,8 @@ struct LoraExpand {
   int col_blocks;
 };
 
-// A tile's rank values into LDS: the splits' parts added in order (four loads in
-// flight), scaled and split into two bf16 parts, the high one at the start of a
+// A tile's rank values into LDS: the splits' parts added in order (eight loads in
+// flight, the last one again past the end), scaled and split into two bf16 parts, the high one at the start of a
 // row of `stride` elements and the low one at `lo`, zeros behind either up to
 // `lo` and `len`; rows past the tile are zeros.  The block with `keep` writes v_out.
 __device__ __forceinline__ void stage_ranks(const LoraExpand& p, const LoraTile& tl, int rows,
@@ -308,15 +308,20 @@ __device__ __forceinline__ void stage_ranks(const LoraExpand& p, const LoraTile&
     if (row < tl.n) {
       const float* src = p.part + (size_t)(tl.p0 + row) * p.r + j;
       const size_t ld = (size_t)p.T * p.r;
-      int k = 0;
-      for (; k + 4 <= p.splits; k += 4) {
-        f32x4 o[4];
+      if (p.splits <= 2) {
+        v = *reinterpret_cast<const f32x4*>(src);
+        if (p.splits == 2) v += *reinterpret_cast<const f32x4*>(src + ld);
+      } else {
+        for (int k = 0; k < p.splits; k += 8) {
+          f32x4 o[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const f32x4*>(src + (k + q) * ld);
+          for (int q = 0; q < 8; ++q)
+            o[q] = *reinterpret_cast<const f32x4*>(src + min(k + q, p.splits - 1) * ld);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v += o[q];
+          for (int q = 0; q < 8; ++q)
+            if (k + q < p.splits) v += o[q];
+        }
       }
-      for (; k < p.splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * ld);
       const f32x4 sv = v * sc;
       if (p.v_out && keep)
         *reinterpret_cast<f32x4*>(p.v_out + (size_t)(tl.p0 + row) * p.r + j) = p.scale_v ? sv : v;
