@@ -37,6 +37,7 @@ namespace moe {
 
 static constexpr int LORA_MAX_RANK = 128;
 static constexpr int LORA_WAVES = 4;
+static constexpr int WGRAD_COLS = 64;     // columns of a block of the weight gradients
 
 // A tile of at most `tm` rows of one adapter's segment (adapter NA: the rows
 // behind the last segment), or n == -1 past the last tile.
@@ -658,20 +659,26 @@ __device__ __forceinline__ int lora_slot(int p0, int segment, int chunk) {
 // read transposed: the reduction runs over rows), u is split into three bf16
 // parts, which hold its 24 bits, so the float32 sums are of float32 accuracy
 // at three bf16 MFMAs a step: 830 TFLOP/s of the bf16 rate against 157 of
-// v_mfma_f32.
+// v_mfma_f32.  Both gradients of 8192 rows of 8 adapters, rank 16, 4096 x 4096:
+// 30 us, 4.7 TB/s, bound by memory; at rank 64 the splitting of u, which every
+// column block repeats, takes as long as the loads (128 columns a block halve it
+// but leave too few waves: 5 to 15 % slower at every size tried).
 template <int RT>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraWgrad p) {
-  constexpr int XS = 64 + 8;
-  __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][XS];
-  __shared__ float red[LORA_WAVES][16][64 + 4];
+  constexpr int CT = WGRAD_COLS / 16, COLS = WGRAD_COLS;
+  constexpr int CPR = COLS / 8, NX = CPR / 2;      // chunks per row, loads per step
+  constexpr int RPI = 64 / CPR;                    // rows per load instruction
+  __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][COLS + 8];
+  __shared__ float red[LORA_WAVES][16][COLS + 4];
   const LoraGrad& G = p.g[blockIdx.z & 1];
-  const int c0 = blockIdx.x * 64, r0 = (blockIdx.z >> 1) * 16 * RT;
+  const int c0 = blockIdx.x * COLS, r0 = (blockIdx.z >> 1) * 16 * RT;
   if (!G.out || c0 >= G.C) return;
   const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.y);
   if (tl.n < 0 || tl.a >= p.NA) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & 15, g = lane >> 4;
-  const int xc = min(c0 + 8 * (lane & 7), G.C - 8);       // (C a multiple of 32)
+  const int xrow = lane / CPR, xcol = 8 * (lane % CPR);
+  const int xc = min(c0 + xcol, G.C - 8);       // (C a multiple of 32)
   // the tokens of 32 rows, one a lane (both halves of the wave alike)
   auto tokens = [&](int s) {
     const int i = 32 * s + (lane & 31);
@@ -681,16 +688,16 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   const u32x4 zero = {0, 0, 0, 0};
   // (every load is issued, rows without a token read row 0 and become zero on
   // their way to LDS: the compiler can then count the loads in flight)
-  auto fetch = [&](int tok, u32x4 (&x)[4]) {
+  auto fetch = [&](int tok, u32x4 (&x)[NX]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = __shfl(tok, 8 * i + (lane >> 3), 64);
+    for (int i = 0; i < NX; ++i) {
+      const int t = __shfl(tok, RPI * i + xrow, 64);
       x[i] = *reinterpret_cast<const u32x4*>(G.x + (size_t)max(t, 0) * G.C + xc);
     }
   };
-  f32x4 acc[RT][4] = {};
+  f32x4 acc[RT][CT] = {};
   const int steps = (tl.n + 31) / 32;
-  u32x4 x[4];
+  u32x4 x[NX];
   int tok = -1, next = -1;
   if (wave < steps) {           // (an adapter without rows reads nothing)
     tok = tokens(wave);
@@ -701,9 +708,9 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
     const uint32_t valid = (uint32_t)__ballot(tok >= 0);
     wave_fence();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x4*>(&xs[wave][8 * i + (lane >> 3)][8 * (lane & 7)]) =
-          valid >> (8 * i + (lane >> 3)) & 1 ? x[i] : zero;
+    for (int i = 0; i < NX; ++i)
+      *reinterpret_cast<u32x4*>(&xs[wave][RPI * i + xrow][xcol]) =
+          valid >> (RPI * i + xrow) & 1 ? x[i] : zero;
     wave_fence();
     // (u's loads in front of the next rows': loads return in order)
     const float* u = G.u + (size_t)(tl.p0 + 32 * s) * p.r;
@@ -717,15 +724,23 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
     tok = next;
     fetch(tok, x);
     next = tokens(s + 2 * LORA_WAVES);
-    u32x4 xa[4];
+    u32x4 xa[CT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const u32x2 v = read_tr(&xs[wave][8 * g + 4 * h + (l >> 2)][16 * i + 4 * (l & 3)]);
         xa[i][2 * h] = v[0];
         xa[i][2 * h + 1] = v[1];
       }
+    // rows without a token, and ranks past r, count as zero
+    if (valid != 0xffffffffu || r0 + 16 * RT > p.r) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + 16 * j + l >= p.r || !(valid >> (8 * g + i) & 1)) uv[j][i] = 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       u32x4 part[3];
@@ -734,8 +749,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
         uint32_t b[3][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v =
-              r0 + 16 * j + l < p.r && (valid >> (8 * g + 2 * q + e) & 1) ? uv[j][2 * q + e] : 0.0f;
+          float v = uv[j][2 * q + e];
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             b[k][e] = bf16_of(v);
@@ -746,7 +760,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
         for (int k = 0; k < 3; ++k) part[k][q] = b[k][0] | b[k][1] << 16;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < CT; ++i)
 #pragma unroll
         for (int k = 0; k < 3; ++k) acc[j][i] = mfma16(part[k], xa[i], acc[j][i]);
     }
@@ -761,12 +775,12 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   for (int j = 0; j < RT; ++j) {
     if (j) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) red[wave][4 * g + q][16 * i + l] = acc[j][i][q];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 64; i += 64 * LORA_WAVES) {
-      const int rr = G.trans ? i % 16 : i / 64, cc = G.trans ? i / 16 : i % 64;
+    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * LORA_WAVES) {
+      const int rr = G.trans ? i % 16 : i / COLS, cc = G.trans ? i / 16 : i % COLS;
       const int rank = r0 + 16 * j + rr, c = c0 + cc;
       if (rank < p.r && c < G.C) {
         float v = 0.0f;
@@ -911,7 +925,8 @@ static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   // up to four rank tiles a block: with eight, one wave per SIMD is left, and
   // nothing covers its waits (2000 rows of rank 128: 58 us against 38)
   const int tiles = (p.r + 15) / 16, rt = tiles <= 4 ? tiles : tiles <= 6 ? 3 : 4;
-  const dim3 grid((wide + 63) / 64, p.T / p.chunk + p.NA + 1, 2 * ((tiles + rt - 1) / rt));
+  const dim3 grid((wide + WGRAD_COLS - 1) / WGRAD_COLS, p.T / p.chunk + p.NA + 1,
+                  2 * ((tiles + rt - 1) / rt));
   const dim3 block(64 * LORA_WAVES);
   switch (rt) {
     case 1: hipLaunchKernelGGL((lora_wgrad_kernel<1>), grid, block, 0, s, p); break;
