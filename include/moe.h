@@ -610,7 +610,8 @@ moe_status_t moe_unpermute_combine_bwd(const void* d_out, const void* y, int dty
  * With row_map no output may share memory with y; outputs never overlap each
  * other, nor an input except as the very same tensor.  dtype MOE_F32 or
  * MOE_BF16; d * element size a multiple of 16, at most 65536 bytes
- * (MOE_ERR_UNSUPPORTED above); eps > 0. */
+ * (MOE_ERR_UNSUPPORTED above); T < 2^31 - 2^20, T * k < 2^31; eps > 0.  The mean
+ * squares are float32: rows of magnitudes past 1e19 overflow them. */
 typedef struct {
   size_t struct_size; /* = sizeof(moe_block_norm_fwd_args_t) */
   int dtype;
@@ -644,7 +645,9 @@ moe_status_t moe_block_norm_fwd(const moe_block_norm_fwd_args_t* args, void* str
  *   dx itself); dw_pre, dw_post, dgate [d] and drow_gate [T] float32 (out,
  *   nullable).  `accumulate` adds the three channel gradients (not drow_gate)
  *   to the existing values.  ws: moe_block_norm_bwd_workspace_size(T, d) bytes,
- *   needed with dw_pre, dw_post or dgate (else MOE_ERR_WORKSPACE). */
+ *   needed with dw_pre, dw_post or dgate (else MOE_ERR_WORKSPACE); its contents
+ *   need no clearing, but calls that may overlap (other streams, graphs replayed
+ *   side by side) need one each.  The same inputs give the same bits. */
 typedef struct {
   size_t struct_size; /* = sizeof(moe_block_norm_bwd_args_t) */
   int dtype;
@@ -721,7 +724,8 @@ moe_status_t moe_clip_grad_norm(const moe_tensor_t* tensors, int n, double max_n
  *     without an adapter are not written.
  *   src_row, if given, a permutation of [0, T); entries outside [0, T) are
  *     skipped.  out may be y; it overlaps nothing else.
- *   ws: moe_lora_workspace_size(T, K, N, r, NA) bytes (both directions).
+ *   ws: moe_lora_workspace_size(T, K, N, r, NA) bytes (both directions); no
+ *     clearing, one for each of calls that may overlap.
  * K and N multiples of 32 up to 2^20, T up to 2^30, r a multiple of 8 up to 128
  * (more: MOE_ERR_UNSUPPORTED), 1 <= NA < MOE_MAX_EXPERTS. */
 typedef struct {

@@ -22,6 +22,16 @@
 // The channel gradients are summed per thread over the rows a block walks
 // (each thread owns fixed columns), written as one float32 row per block and
 // added in block order by a second kernel: no atomics, the same bits each run.
+//
+// Both directions are bound by HBM (a large copy on the card: 4.9 TB/s), and the
+// counters show each tensor moved once.  Measured at 16384 x 7168 bf16, both norms
+// and a channel gate: forward 167 us = 5.6 TB/s, backward 296 us = 4.8 TB/s with
+// the channel sums; with 4 expert rows combined, 8191 x 2880: 56 us = 5.9 TB/s; one
+// row to a few: 5 us forward, 10 backward, a chain of loads and two reductions.
+// What carried it: a row's loads issued while the row before is reduced (the
+// forward's first form, a block a row, took 270 us), channel vectors in registers
+// for all rows of a block, one chunk a lane (two a lane spill the backward: 997
+// us), the hardware's bf16 conversion, and 8 to 16 waves per compute unit.
 #include "common.hpp"
 #include "spans.hpp"
 
@@ -163,7 +173,8 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
 
 // Blocks walk the rows; a row's loads are issued while the one before it is
 // reduced, and the channel vectors stay in registers throughout.  STREAM: h1 and
-// x are stored nontemporally, where they are larger than the L2 anyway.
+// x are stored nontemporally, where they are larger than the L2 anyway (16384 x
+// 2880: 63 us against 71; the backward gains nothing from it).
 template <class EL, int NC, int LPR, bool POST, bool PRE, bool COMB, bool STREAM>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
   constexpr int V = EL::VEC;
@@ -482,6 +493,10 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const NormFinis
 struct NormGeom {
   int nc, lpr, waves;
 };
+// Rows of up to 64 chunks share a wave where they can (16384 x 64: backward 9.9 us,
+// a wave a row 18.6); the combine, whose expert rows are not loaded ahead, takes
+// two chunks a lane to have more loads in flight (8191 x 2880, 4 rows: 59 us, one
+// chunk 65).
 static NormGeom norm_geom(int chunks, bool comb = false) {
   if (chunks <= 8) return {1, 8, 0};
   if (chunks <= 16) return {1, 16, 0};
