@@ -681,7 +681,7 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* args, void* str
  * Squares are summed in float64 in a fixed order, the norm is rounded to float32
  * once; c is computed in float64 and rounded to float32 once; data * c is a
  * float32 product, rounded once to out's type.  A norm of
- * infinity gives c = 0, a NaN norm gives NaN everywhere.
+ * infinity gives c = 0 (max_norm finite), a NaN norm gives NaN everywhere.
  *   tensors [n]: a HOST array, read during the call only; data and out are
  *     device pointers aligned to their element size; numel may be 0; dtype and
  *     out_dtype are MOE_F32 or MOE_BF16.  moe_grad_norm reads data, numel and
@@ -692,7 +692,7 @@ moe_status_t moe_block_norm_bwd(const moe_block_norm_bwd_args_t* args, void* str
  *   norm: float32 device word (out).
  *   ws: moe_grad_norm_workspace_size(n) bytes, 16-byte aligned; its contents
  *     need no clearing, but calls that may overlap need one each.
- * max_norm >= 0 (infinity: never clips), eps > 0. */
+ * max_norm >= 0 (infinity: c = 1 unless the norm is NaN), eps > 0. */
 typedef struct {
   const void* data;
   void* out;

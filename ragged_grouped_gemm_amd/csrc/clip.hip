@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_scale_kernel(const ClipBatc
   __shared__ double lds[CLIP_THREADS / 64];
   const double nv = norm_of_slots(slots, nslots, lds);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)nv;
-  const double cd = max_norm / (nv + eps);
+  // (an infinite max_norm never clips, an infinite norm neither)
+  const double cd = isinf(max_norm) && isinf(nv) ? 1.0 : max_norm / (nv + eps);
   const float c = cd >= 1.0 ? 1.0f : (float)cd;       // a NaN norm gives NaN everywhere
   for (int i = blockIdx.x; i < b.pieces; i += gridDim.x) {
     const int k = find_tensor(b, i);

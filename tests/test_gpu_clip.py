@@ -158,3 +158,44 @@ def test_graph_replay_between_eager_calls():
         eager = [torch.empty_like(t) for t in out]
         n2 = ops.moe_clip_grad_norm(gr, max_norm, out=eager)
         assert torch.equal(n2, norm) and all(torch.equal(a, b) for a, b in zip(eager, out))
+
+
+def test_infinite_max_norm_only_measures():
+    """Nothing is scaled, whatever the norm, so long as it is a number."""
+    from ragged_grouped_gemm_amd import ops
+    note("clip infinite max_norm")
+    a = torch.tensor([1.0, math.inf, -3.0], device="cuda")
+    out = torch.full_like(a, 7.0)
+    assert math.isinf(float(ops.moe_clip_grad_norm([a], math.inf, out=[out])))
+    assert torch.equal(out, a)
+    assert math.isinf(float(ops.moe_clip_grad_norm([a], math.inf)))
+    assert torch.equal(out, a)
+    a[0] = math.nan
+    assert math.isnan(float(ops.moe_clip_grad_norm([a], math.inf)))
+    assert torch.isnan(a).all()
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, on inputs made on a third."""
+    from ragged_grouped_gemm_amd import ops
+    note("clip two streams")
+    sizes = [300001, 5, 40000]
+    sets = [_make(sizes, ["f32", "bf16", "f32"], 20 + i) for i in range(2)]
+    max_norm = [0.4 * _norm64(s) for s in sets]
+    want = []
+    for s, m in zip(sets, max_norm):
+        o = [torch.empty_like(t) for t in s]
+        want.append((ops.moe_clip_grad_norm(s, m, out=o), o))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                o = [torch.empty_like(t) for t in sets[i]]
+                got[i].append((ops.moe_clip_grad_norm(sets[i], max_norm[i], out=o), o))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for n, o in got[i]:
+            assert torch.equal(n, want[i][0]) and all(torch.equal(a, b) for a, b in zip(o, want[i][1]))

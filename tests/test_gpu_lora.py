@@ -275,3 +275,30 @@ def test_empty_batch_gives_zero_weight_gradients():
     dx, dA, dB = ops.moe_lora_bwd(x, y, A, B, off, v, dA=torch.full(A.shape, 3.0, device="cuda"))
     assert dx.shape == (0, 64) and not dA.any() and not dB.any()
     ops.moe_lora_bwd(x, y, A, B, off, v, want_dw=False)
+
+
+@pytest.mark.parametrize("T,N", [(40, 256), (1500, 1024)])
+def test_two_streams_at_once(T, N):
+    """Calls in flight on two streams that share the adapters and the plan, each with its own
+    workspace, give the bits of calls made alone (T = 40 and 1500: the kernels for few and for
+    many rows)."""
+    note(f"lora two streams T={T}")
+    c = [Case(T, 256, N, 16, 3, seed=s) for s in (1, 2)]
+    for n in ("A", "B", "sc", "off", "src"):
+        setattr(c[1], n, getattr(c[0], n))
+    def both(k):
+        out, v = k.forward(out=torch.empty_like(k.y[1]), want_v=True)
+        return [out, v, *k.backward(v, dx=k.dx[1], dx_out=torch.empty_like(k.dx[1]))]
+    want = [both(k) for k in c]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(6):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(both(c[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
