@@ -128,6 +128,7 @@ class MoEFFN:
         self.W1p_saved = self.b1p_saved = None
         self.fuse_permute = fuse_permute and not self.mx and self.gather_fits(T, d, dtype)
         self.x_saved = None
+        self.forwards = 0        # how many, so that a block can tell whose rows are here
         if self.mx and (bias or act == "srelu" or dtype != torch.bfloat16):
             raise ValueError("the MXFP8 variant is gated, bias-free, with bf16 activations")
         if router and dtype != torch.bfloat16:
@@ -269,6 +270,7 @@ class MoEFFN:
     def forward_rows(self, x, logits, W1p, W2, b1p=None, b2=None):
         """The forward up to the expert rows Y [R, d], before the combine
         (out[t] = sum_j combine_weights()[t, j] Y[row_map[t, j]])."""
+        self.forwards += 1
         if self.mx:
             return self._forward_mx(x, logits, W1p)
         self._route(x, logits)
@@ -466,7 +468,9 @@ class MoEBlock:
     optional.  The combine of the expert rows, the norm after the layer, gate,
     residual and the next block's norm are one launch (moe_block_norm_fwd), and
     one more goes back through them (moe_block_norm_bwd).  ``ffn`` is a MoEFFN
-    of any variant; the block adds buffers from the same ``alloc``.
+    of any variant; the block adds buffers from the same ``alloc``.  Blocks may
+    share one without backward buffers; a backward needs the layer's own forward
+    to be its last.
 
     Stacked blocks pass (h1, x') on and (dh, dX) back:
         h, x = a.forward(h, x, ..., next_w_pre=w_b)
@@ -498,10 +502,15 @@ class MoEBlock:
     def forward(self, h, x, logits, W1p, W2, b1p=None, b2=None, *, w_pre=None, w_post=None,
                 gate=None, next_w_pre=None):
         """Returns (h1, x' or None).  logits, W1p, W2, b1p, b2 as MoEFFN.forward.
-        h, and x or the weights, must not change before the backward."""
+        The backward reads again what the pre-norm or the layer read (h with
+        w_pre, else x), so that must not change, nor be one of this block's outputs."""
         L = self.ffn
         if (x is None) == (w_pre is None):
             raise ValueError("give the block either its normed input x or its norm's weight w_pre")
+        kept = h if x is None else x
+        if L.has_backward and any(kept.data_ptr() == t.data_ptr()
+                                  for t in (self.h1, self.x_next, self.y)):
+            raise ValueError("the block would write over its input, which the backward reads")
         if x is None:
             with L._op("norm_pre"):
                 x = ops.moe_block_norm_fwd(h, w_pre=w_pre, eps=self.eps, x_out=self.x_own)[1]
@@ -512,7 +521,7 @@ class MoEBlock:
                 eps=self.eps, row_map=L.row_map, topk_w=L.combine_weights(), h_out=self.h1,
                 x_out=self.x_next if next_w_pre is not None else None,
                 y_out=self.y if L.has_backward else None)
-        self.saved = (h, w_pre, w_post, gate, next_w_pre)
+        self.saved = (L.forwards, h, w_pre, w_post, gate, next_w_pre)
         return self.h1, xn
 
     def backward(self, dh1, dx_next, logits, W1p, W2):
@@ -524,7 +533,9 @@ class MoEBlock:
             raise RuntimeError("layer built without backward buffers")
         if self.saved is None:
             raise RuntimeError("backward before forward")
-        h, w_pre, w_post, gate, next_w_pre = self.saved
+        turn, h, w_pre, w_post, gate, next_w_pre = self.saved
+        if turn != L.forwards:
+            raise RuntimeError("the layer ran another forward since this block's")
         used = dx_next is not None
         if used and next_w_pre is None:
             raise ValueError("the forward made no input for a next block")

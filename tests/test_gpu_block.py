@@ -207,3 +207,37 @@ def test_block_refuses_what_it_cannot_do():
         b.clip_grads(1.0)
     with pytest.raises(RuntimeError, match="without backward"):
         MoEBlock(MoEFFN(8, 64, 32, 4, 2, backward=False)).backward(t, None, None, None, None)
+
+
+def test_block_refuses_backward_of_overwritten_state():
+    """Inputs that the block's own outputs replace, and a layer that ran again in between."""
+    from ragged_grouped_gemm_amd import ops
+    from ragged_grouped_gemm_amd.layer import MoEBlock, MoEFFN
+    note("block overwritten state")
+    T, d, f, E, k = 8, 64, 32, 4, 2
+    r = lambda *s: torch.randn(s, device="cuda").bfloat16()
+    W1p, _ = ops.moe_repack_glu_weights(r(E, 2 * f, d))
+    args = (torch.randn(T, E, device="cuda"), W1p, r(E, d, f))
+    w = torch.ones(d, device="cuda")
+    L = MoEFFN(T, d, f, E, k)
+    a, b = MoEBlock(L), MoEBlock(L)
+    h1, x = a.forward(r(T, d), None, *args, w_pre=w, next_w_pre=w)
+    with pytest.raises(ValueError, match="write over"):
+        a.forward(h1, None, *args, w_pre=w, next_w_pre=w)
+    with pytest.raises(ValueError, match="write over"):
+        a.forward(h1, x, *args, next_w_pre=w)
+    h = r(T, d)
+    h2, _ = a.forward(h, None, *args, w_pre=w)
+    keep = h2.clone()
+    b.forward(h, None, *args, w_pre=w)
+    with pytest.raises(RuntimeError, match="another forward"):
+        a.backward(r(T, d), None, *args)
+    b.backward(r(T, d), None, *args)
+    # without a backward, blocks share a layer, and a residual stream stays in one buffer
+    L = MoEFFN(T, d, f, E, k, backward=False)
+    a = MoEBlock(L)
+    h2, _ = a.forward(h, None, *args, w_pre=w)
+    assert torch.equal(h2, keep)
+    want, _ = MoEBlock(L).forward(keep, None, *args, w_pre=w)
+    h3, _ = a.forward(h2, None, *args, w_pre=w)
+    assert h3.data_ptr() == h2.data_ptr() and torch.equal(h3, want)
