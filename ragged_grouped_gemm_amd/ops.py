@@ -7,8 +7,9 @@ passed in (preallocated, e.g. for graph capture) or are allocated here.
 """
 from __future__ import annotations
 
-import array
 import ctypes
+import itertools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -676,6 +677,17 @@ def moe_block_norm_bwd(h1, y=None, *, dh1=None, dx=None, w_post=None, gate=None,
     return BlockNormGrads(dh, dy, dw_post, dgate, drow_gate, dw_pre)
 
 
+def _kinds(tensors):
+    """The library's codes of the tensors' types (mostly one type, which costs less to find)."""
+    types = list(map(torch.Tensor.dtype.__get__, tensors))
+    try:
+        if len(set(types)) == 1:
+            return [_DT[types[0]]] * len(types)
+        return [_DT[t] for t in types]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]} (float32 or bfloat16)") from None
+
+
 def _tensor_list(grads, out):
     """The ctypes moe_tensor_t array of the tensors (out: None, or one tensor per gradient)."""
     n = len(grads)
@@ -694,17 +706,11 @@ def _tensor_list(grads, out):
     if out is not None and numels != list(map(torch.Tensor.numel, out)):
         raise ValueError("out must have as many elements as the tensors")
     ptrs = list(map(torch.Tensor.data_ptr, tensors))
-    try:
-        kinds = [_DT[t.dtype] for t in tensors]
-    except KeyError as e:
-        raise TypeError(f"unsupported dtype {e.args[0]} (float32 or bfloat16)") from None
-    # moe_tensor_t is four 8-byte words: data, out, numel, dtype | out_dtype << 32
-    words = array.array("q", bytes(32 * n))
-    words[0::4] = array.array("q", ptrs[:n])
-    words[1::4] = array.array("q", ptrs[-n:])
-    words[2::4] = array.array("q", numels)
-    words[3::4] = array.array("q", [a | b << 32 for a, b in zip(kinds, kinds[-n:])])
-    return (_lib.TensorT * n).from_buffer(words), n, dev
+    kinds = _kinds(grads)
+    # the fields of moe_tensor_t in order (packed at once: field by field costs three times that)
+    fields = zip(ptrs[:n], ptrs[-n:], numels, kinds, kinds if out is None else _kinds(out))
+    raw = struct.pack("qqqii" * n, *itertools.chain.from_iterable(fields))
+    return (_lib.TensorT * n).from_buffer_copy(raw), n, dev
 
 
 def moe_grad_norm_workspace_size(n) -> int:
