@@ -30,8 +30,8 @@
 // row to a few: 5 us forward, 10 backward, a chain of loads and two reductions.
 // What carried it: a row's loads issued while the row before is reduced (the
 // forward's first form, a block a row, took 270 us), channel vectors in registers
-// for all rows of a block, one chunk a lane (two a lane spill the backward: 997
-// us), the hardware's bf16 conversion, and 8 to 16 waves per compute unit.
+// for all rows of a block, one chunk a lane where a row fits, the hardware's bf16
+// conversion, and 8 to 16 waves per compute unit.
 #include "common.hpp"
 #include "spans.hpp"
 
@@ -172,13 +172,14 @@ __device__ __forceinline__ void combine_chunk(const NormFwd& p, int t, int c, fl
 }
 
 // Blocks walk the rows; a row's loads are issued while the one before it is
-// reduced, and the channel vectors stay in registers throughout.  STREAM: h1 and
+// reduced (not with 32 elements a thread, which would spill: 2048 x 32768 bf16 161 us,
+// 247 ahead), and the channel vectors stay in registers throughout.  STREAM: h1 and
 // x are stored nontemporally, where they are larger than the L2 anyway (16384 x
 // 2880: 63 us against 71; the backward gains nothing from it).
 template <class EL, int NC, int LPR, bool POST, bool PRE, bool COMB, bool STREAM>
 __global__ void __launch_bounds__(LPR ? 256 : 1024) block_norm_fwd_kernel(const NormFwd p) {
   constexpr int V = EL::VEC;
-  constexpr bool LOADY = POST && !COMB;
+  constexpr bool LOADY = POST && !COMB, AHEAD = NC * V <= 16;
   __shared__ f32x4 lds[2][16];
   const NormPlace<LPR> pl;
   const int lt = pl.lt, TPR = pl.tpr, rpb = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) block_norm_fwd_kernel(const 
       if constexpr (LOADY) yr[i] = in[i] && row < p.T ? p.y[o] : zero;
     }
   };
-  fetch(t);
+  if constexpr (AHEAD) fetch(t);
   float wg[NC][V], wp[NC][V];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -218,12 +219,13 @@ __global__ void __launch_bounds__(LPR ? 256 : 1024) block_norm_fwd_kernel(const 
   for (; t < p.T; t += step) {
     const size_t row = (size_t)t * p.chunks + lt;
     float h[NC][V], y[NC][V];
+    if constexpr (!AHEAD) fetch(t);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       unpack_chunk(hr[i], h[i], EL());
       if constexpr (LOADY) unpack_chunk(yr[i], y[i], EL());
     }
-    fetch(t + step);
+    if constexpr (AHEAD) fetch(t + step);
     if constexpr (POST) {
       float s[1] = {0.0f};
 #pragma unroll
@@ -278,6 +280,10 @@ constexpr int norm_bwd_threads(int nc, int lpr, int waves) {
   return lpr == 0 ? 64 * waves : lpr == 64 ? (nc == 1 ? 1024 : 512) : 256;
 }
 
+// Keeps the compiler from holding a chunk's floats across a reduction, where its
+// 16 bytes are enough and registers are short.
+__device__ __forceinline__ void unpack_again(u32x4& c) { asm volatile("" : "+v"(c)); }
+
 struct NormBwd {
   const u32x4 *h1, *y, *dh1, *dx;
   const float *w_post, *gate, *row_gate, *w_pre;
@@ -288,11 +294,22 @@ struct NormBwd {
   float res_scale, eps, inv_d;
 };
 
+// A thread owns its columns' channel sums.  They are registers where a lane has one
+// chunk or a wave has the row, else LDS, which wider rows would otherwise spill
+// (4096 x 16384 bf16: 207 us, 567 with spilled sums); bf16 rows of more than 16384
+// have room there for those of the norm in front only, those of y stay in the
+// workspace.  Threads with 16 elements of a row or more do not load the next one
+// ahead (207 us, 317 ahead): the registers that are left hold one row, and a row is
+// long enough to cover most of the wait.
 template <class EL, int NC, int LPR, bool POST, bool PRE>
 __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_kernel(
     const NormBwd p) {
   constexpr int V = EL::VEC;
+  constexpr bool WIDE = LPR == 0 && NC > 1, AHEAD = !WIDE || NC * V <= 8;
+  constexpr bool POST_OUT = NC * V > 16 && PRE && POST;      // sums of y in the workspace
+  constexpr int SLOTS = NC * 1024, SETS = WIDE ? PRE + POST - POST_OUT : 0;
   __shared__ f32x4 lds[2][16];
+  __shared__ f32x4 sums[SETS ? SETS * (V / 4) * SLOTS : 1];  // [set][V / 4][chunk]
   const NormPlace<LPR> pl;
   const int lt = pl.lt, TPR = pl.tpr, rpb = LPR ? blockDim.x / (LPR ? LPR : 1) : 1;
   const int step = gridDim.x * rpb;
@@ -315,14 +332,51 @@ __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_
     }
   };
   int t = blockIdx.x * rpb + pl.sub;
-  fetch(t);
-  float wg[NC][V], wp[NC][V], apre[NC][V], apost[NC][V];
+  if constexpr (AHEAD) fetch(t);
+  constexpr int AC = WIDE ? 1 : NC;
+  float wg[NC][V], wp[NC][V], apre[AC][V], apost[AC][V];
+  // where four sums (q = 0 or 4) of this thread's chunk i live
+  const auto sum4 = [&](bool post, int i, int q) -> f32x4* {
+    if (post && POST_OUT)
+      return reinterpret_cast<f32x4*>(p.part_post + ((size_t)blockIdx.x * p.chunks + lt + i * TPR) * V + q);
+    return sums + ((post && PRE) * (V / 4) + q / 4) * SLOTS + lt + i * TPR;
+  };
+  // adds a[q] b[q] to the sums of chunk i
+  auto add = [&](auto post, float (&acc)[AC][V], int i, const float* a, const float* b) {
+    constexpr bool P = decltype(post)::value;
+    if constexpr (WIDE) {
+      if (!in[i] || !(P ? p.part_post : p.part_pre)) return;
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        f32x4* at = sum4(P, i, q);
+        f32x4 v = *at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(a[q + e], b[q + e], v[e]);
+        *at = v;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[i][q] = fmaf(a[q], b[q], acc[i][q]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < AC; ++i)
+#pragma unroll
+    for (int q = 0; q < V; ++q) apre[i][q] = apost[i][q] = 0.0f;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) wg[i][q] = wp[i][q] = apre[i][q] = apost[i][q] = 0.0f;
+    for (int q = 0; q < V; ++q) wg[i][q] = wp[i][q] = 0.0f;
     if (in[i]) {
       const int c = lt + i * TPR;
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int q = 0; q < V; q += 4) {
+          const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (PRE) *sum4(false, i, q) = none;
+          if (POST && (!POST_OUT || p.part_post)) *sum4(true, i, q) = none;
+        }
+      }
       if constexpr (POST) {
         float g[V];
         load_chan<V>(p.w_post, c, wg[i], 1.0f);
@@ -335,40 +389,60 @@ __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_
   }
   for (; t < p.T; t += step) {
     const size_t row = (size_t)t * p.chunks + lt;
-    float D[NC][V], h[NC][V], z[NC][V], y[NC][V];
+    u32x4 hc[NC], zc[NC], yc[NC], gc[NC];
+    if constexpr (!AHEAD) fetch(t);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) hc[i] = hr[i], zc[i] = zr[i], yc[i] = yr[i], gc[i] = gr[i];
+    if constexpr (AHEAD) fetch(t + step);
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      unpack_chunk(gr[i], D[i], EL());
+      float h[V], z[V], y[V];
       if constexpr (PRE) {
-        unpack_chunk(hr[i], h[i], EL());
-        unpack_chunk(zr[i], z[i], EL());
+        unpack_chunk(hc[i], h, EL());
+        unpack_chunk(zc[i], z, EL());
       }
-      if constexpr (POST) unpack_chunk(yr[i], y[i], EL());
-    }
-    fetch(t + step);
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
+      if constexpr (POST) unpack_chunk(yc[i], y, EL());
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         if constexpr (PRE) {
-          s[0] = fmaf(h[i][q], h[i][q], s[0]);
-          s[1] = fmaf(z[i][q] * wp[i][q], h[i][q], s[1]);
+          s[0] = fmaf(h[q], h[q], s[0]);
+          s[1] = fmaf(z[q] * wp[i][q], h[q], s[1]);
         }
-        if constexpr (POST) s[2] = fmaf(y[i][q], y[i][q], s[2]);
+        if constexpr (POST) s[2] = fmaf(y[q], y[q], s[2]);
       }
+    }
     if (PRE || p.w_post) row_sums<3, LPR>(s, lds, 0);
-    if constexpr (PRE) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if constexpr (PRE) {
+          unpack_again(hc[i]);
+          unpack_again(zc[i]);
+        }
+        if constexpr (POST) unpack_again(yc[i]);
+      }
+    }
+    float D[NC][V];
+    {
       const float r = 1.0f / sqrtf(s[0] * p.inv_d + p.eps);
       const float m = -r * r * (s[1] * p.inv_d);
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int i = 0; i < NC; ++i) {
+        unpack_chunk(gc[i], D[i], EL());
+        if constexpr (PRE) {
+          float h[V], z[V], hn[V];
+          unpack_chunk(hc[i], h, EL());
+          unpack_chunk(zc[i], z, EL());
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          const float zw = z[i][q] * wp[i][q];
-          apre[i][q] = fmaf(z[i][q], h[i][q] * r, apre[i][q]);
-          D[i][q] = fmaf(r, fmaf(h[i][q], m, zw), D[i][q]);
+          for (int q = 0; q < V; ++q) {
+            const float zw = z[q] * wp[i][q];
+            hn[q] = h[q] * r;
+            D[i][q] = fmaf(r, fmaf(h[q], m, zw), D[i][q]);
+          }
+          add(std::false_type(), apre, i, z, hn);
         }
+      }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -382,21 +456,28 @@ __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_
       const float f = ry * (p.row_gate ? p.row_gate[t] : 1.0f);
       float s2[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+      for (int i = 0; i < NC; ++i) {
+        float y[V], yf[V];
+        unpack_chunk(yc[i], y, EL());
+#pragma unroll
+        for (int q = 0; q < V; ++q) yf[q] = y[q] * f;
+        add(std::true_type(), apost, i, D[i], yf);
 #pragma unroll
         for (int q = 0; q < V; ++q) {
-          apost[i][q] = fmaf(D[i][q], y[i][q] * f, apost[i][q]);
           D[i][q] *= wg[i][q];
-          s2[0] = fmaf(D[i][q], y[i][q], s2[0]);
+          s2[0] = fmaf(D[i][q], y[q], s2[0]);
         }
+      }
       if (p.w_post || p.drow_gate) row_sums<1, LPR>(s2, lds, 1);
       if (p.drow_gate && lt == 0) p.drow_gate[t] = ry * s2[0];
       const float m = p.w_post ? -f * (ry * ry * (s2[0] * p.inv_d)) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        float o[V];
+        if constexpr (WIDE) unpack_again(yc[i]);
+        float o[V], y[V];
+        unpack_chunk(yc[i], y, EL());
 #pragma unroll
-        for (int q = 0; q < V; ++q) o[q] = fmaf(y[i][q], m, f * D[i][q]);
+        for (int q = 0; q < V; ++q) o[q] = fmaf(y[q], m, f * D[i][q]);
         if (in[i]) p.dy[row + i * TPR] = store_chunk(o, EL());
       }
     }
@@ -405,8 +486,9 @@ __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_
   }
   // one row of sums per block: a wave's rows are added in a butterfly, the waves
   // of a block that holds several rows in order
-  auto put = [&](float* part, float (&a)[NC][V]) {
-    if (!part) return;
+  auto put = [&](auto post, float* part, float (&a)[AC][V]) {
+    constexpr bool P = decltype(post)::value;
+    if (!part || (P && WIDE && POST_OUT)) return;
     float* o = part + (size_t)blockIdx.x * p.chunks * V;
     if constexpr (LPR > 0) {
       __shared__ __align__(16) float acc[NC * LPR * V];
@@ -437,11 +519,15 @@ __global__ void __launch_bounds__(norm_bwd_threads(NC, LPR, 16)) block_norm_bwd_
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int q = 0; q < V; q += 4)
-          if (in[i]) store4(o + (size_t)(lt + i * TPR) * V + q, &a[i][q]);
+          if (in[i]) {
+            float* at = o + (size_t)(lt + i * TPR) * V + q;
+            if constexpr (WIDE) *reinterpret_cast<f32x4*>(at) = *sum4(P, i, q);
+            else store4(at, &a[i][q]);
+          }
     }
   };
-  if constexpr (PRE) put(p.part_pre, apre);
-  if constexpr (POST) put(p.part_post, apost);
+  if constexpr (PRE) put(std::false_type(), p.part_pre, apre);
+  if constexpr (POST) put(std::true_type(), p.part_post, apost);
 }
 
 // The channel gradients from the blocks' rows of sums, added in order: 32 groups

@@ -293,3 +293,18 @@ def test_other_stream_and_graph_replay():
                                    gb["dgate"], gb["drow_gate"], gb["dw_pre"])]
         for a, b in zip(got, c.forward()[:2] + tuple(c.backward())):
             assert torch.equal(a, b), seed
+
+
+@pytest.mark.parametrize("flags", ["ypgx1", "yptx1", "ypgtx", "ygt1", "y1", "yx1", "x"])
+@pytest.mark.parametrize("dtype,T,d", [("bf16", 600, 8200), ("f32", 530, 4100), ("bf16", 300, 20480),
+                                       ("f32", 300, 8256)])
+def test_wide_rows_share_blocks(dtype, T, d, flags):
+    """More rows than blocks, where a thread holds two chunks of a row or four."""
+    note(f"block_norm wide {dtype} T={T} d={d} {flags}")
+    c = Case(T, d, dtype, flags)
+    h1, x, _ = c.forward()
+    c.check_forward(h1, x)
+    r = c.backward()
+    c.check_backward(r)
+    for a, b in zip(r, c.backward()):
+        assert a is b is None or torch.equal(a, b)
