@@ -489,6 +489,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraE
                                                                      const int rows) {
   constexpr int DEPTH = KH <= 2 ? 4 : 2;
   constexpr int VS = 64 * KH + 8;           // a row's two parts of 32 KH ranks
+  constexpr int WS = 64 + 8;                // row stride of a wave's factor tile
+  static_assert(LORA_WAVES * 32 * WS <= apply_rows(KH) * VS, "the factor's tiles fit");
   __shared__ int toks[apply_rows(KH)];
   __shared__ __align__(16) uint16_t vs[apply_rows(KH) * VS];
   const LoraTile tl =
@@ -515,23 +517,46 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_apply_kernel(const LoraE
     bad |= i < tl.n && t < 0;
     toks[i] = t;
   }
+  // (ranks past r: any of the factor's, the rank values are zero there)
   u32x4 wa[KH][4];
   const uint16_t* w = p.w + (size_t)tl.a * p.r * p.C;
+  if constexpr (TRANS) {
+    // whole lines, 8 ranks an instruction, turned in the memory that the rank values
+    // take next, 32 ranks at a time (4096 x 7168 at rank 128: 43 us, 54 with two-byte
+    // loads)
+    uint16_t* wt = vs + wave * 32 * WS;
+    const int cw = min(c0 + 8 * (lane & 7), p.C - 8);
+    u32x4 raw[KH][4];
 #pragma unroll
-  for (int s = 0; s < KH; ++s) {
-    const int j = 32 * s + 8 * g < p.r ? 32 * s + 8 * g : 0;     // past r the rank values are zero
+    for (int k = 0; k < 4 * KH; ++k)
+      raw[k / 4][k % 4] = *reinterpret_cast<const u32x4*>(
+          w + (size_t)min(8 * k + (lane >> 3), p.r - 1) * p.C + cw);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int cw = min(c0 + lora_column(i, l >> 2) + (l & 3), p.C - 1);
-      if constexpr (TRANS) {
+    for (int s = 0; s < KH; ++s) {
+      wave_fence();
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          wa[s][i][q] = (uint32_t)w[(size_t)(j + 2 * q) * p.C + cw] |
-                        (uint32_t)w[(size_t)(j + 2 * q + 1) * p.C + cw] << 16;
-      } else {
-        wa[s][i] = *reinterpret_cast<const u32x4*>(w + (size_t)cw * p.r + j);
-      }
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<u32x4*>(wt + (8 * k + (lane >> 3)) * WS + 8 * (lane & 7)) = raw[s][k];
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x2 v = read_tr(wt + (8 * g + 4 * h + (l >> 2)) * WS + lora_column(i, l & 3));
+          wa[s][i][2 * h] = v[0];
+          wa[s][i][2 * h + 1] = v[1];
+        }
     }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int s = 0; s < KH; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int cw = min(c0 + lora_column(i, l >> 2) + (l & 3), p.C - 1);
+        wa[s][i] = *reinterpret_cast<const u32x4*>(w + (size_t)cw * p.r +
+                                                   min(32 * s + 8 * g, p.r - 8));
+      }
   }
   stage_ranks(p, tl, (tl.n + 15) & ~15, blockIdx.x % p.col_blocks == 0, 32 * KH, 64 * KH, vs, VS);
   const bool plain = __syncthreads_or(bad) || !p.y || c0 + 64 > p.C;
