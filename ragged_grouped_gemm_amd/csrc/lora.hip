@@ -688,19 +688,25 @@ __device__ __forceinline__ int lora_slot(int p0, int segment, int chunk) {
 // 30 us, 4.7 TB/s, bound by memory; at rank 64 the splitting of u, which every
 // column block repeats, takes as long as the loads (128 columns a block halve it
 // but leave too few waves: 5 to 15 % slower at every size tried).
-template <int RT>
+//
+// SHORT: each wave takes 64 columns of its own and every row, for segments that would
+// leave most waves without rows.
+template <int RT, bool SHORT>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraWgrad p) {
   constexpr int CT = WGRAD_COLS / 16, COLS = WGRAD_COLS;
   constexpr int CPR = COLS / 8, NX = CPR / 2;      // chunks per row, loads per step
   constexpr int RPI = 64 / CPR;                    // rows per load instruction
   __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][COLS + 8];
-  __shared__ float red[LORA_WAVES][16][COLS + 4];
+  __shared__ __align__(16) float red[LORA_WAVES][16][COLS + 4];
   const LoraGrad& G = p.g[blockIdx.z & 1];
-  const int c0 = blockIdx.x * COLS, r0 = (blockIdx.z >> 1) * 16 * RT;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c0 = (SHORT ? blockIdx.x * LORA_WAVES + wave : blockIdx.x) * COLS;
+  const int r0 = (blockIdx.z >> 1) * 16 * RT;
   if (!G.out || c0 >= G.C) return;
   const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.y);
   if (tl.n < 0 || tl.a >= p.NA) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int STEP = SHORT ? 1 : LORA_WAVES;
+  const int first = SHORT ? 0 : wave;
   const int l = lane & 15, g = lane >> 4;
   const int xrow = lane / CPR, xcol = 8 * (lane % CPR);
   const int xc = min(c0 + xcol, G.C - 8);       // (C a multiple of 32)
@@ -724,12 +730,12 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   const int steps = (tl.n + 31) / 32;
   u32x4 x[NX];
   int tok = -1, next = -1;
-  if (wave < steps) {           // (an adapter without rows reads nothing)
-    tok = tokens(wave);
+  if (first < steps) {          // (an adapter without rows reads nothing)
+    tok = tokens(first);
     fetch(tok, x);
-    next = tokens(wave + LORA_WAVES);
+    next = tokens(first + STEP);
   }
-  for (int s = wave; s < steps; s += LORA_WAVES) {
+  for (int s = first; s < steps; s += STEP) {
     const uint32_t valid = (uint32_t)__ballot(tok >= 0);
     wave_fence();
 #pragma unroll
@@ -748,7 +754,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
         uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(r0 + 16 * j + l, p.r - 1)];
     tok = next;
     fetch(tok, x);
-    next = tokens(s + 2 * LORA_WAVES);
+    next = tokens(s + 2 * STEP);
     u32x4 xa[CT];
 #pragma unroll
     for (int i = 0; i < CT; ++i)
@@ -796,25 +802,38 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
   float* out = whole ? G.out + (size_t)tl.a * p.r * G.C
                      : G.part + (size_t)lora_slot(tl.p0, tl.s0, p.chunk) * p.r * G.C;
   const bool add = whole && p.accumulate;
+  auto sync = [&]() {
+    if constexpr (SHORT) wave_fence();
+    else __syncthreads();
+  };
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    if (j) __syncthreads();
+    if (j) sync();
 #pragma unroll
     for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) red[wave][4 * g + q][16 * i + l] = acc[j][i][q];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * COLS; i += 64 * LORA_WAVES) {
-      const int rr = G.trans ? i % 16 : i / COLS, cc = G.trans ? i / 16 : i % COLS;
+    sync();
+    // four sums a lane, along the columns or (trans) the ranks
+    for (int i = SHORT ? lane : threadIdx.x; i < 4 * COLS; i += SHORT ? 64 : 64 * LORA_WAVES) {
+      const int rr = G.trans ? i % 4 * 4 : i / (COLS / 4), cc = G.trans ? i / 4 : i % (COLS / 4) * 4;
       const int rank = r0 + 16 * j + rr, c = c0 + cc;
-      if (rank < p.r && c < G.C) {
-        float v = 0.0f;
+      if (rank >= p.r || c >= G.C) continue;
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < LORA_WAVES; ++k) v += red[k][rr][cc];
-        v *= sc;
-        float* o = out + (G.trans ? (size_t)c * p.r + rank : (size_t)rank * G.C + c);
-        *o = add ? *o + v : v;
+      for (int k = 0; k < STEP; ++k) {
+        const float(*from)[COLS + 4] = red[SHORT ? wave : k];
+        if (G.trans) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += from[rr + e][cc];
+        } else {
+          v += *reinterpret_cast<const f32x4*>(&from[rr][cc]);
+        }
       }
+      v *= sc;
+      f32x4* o = reinterpret_cast<f32x4*>(
+          out + (G.trans ? (size_t)c * p.r + rank : (size_t)rank * G.C + c));
+      *o = add ? *o + v : v;
     }
   }
 }
@@ -945,19 +964,30 @@ static size_t lora_slots(int T) {
   return T > lora_chunk(T) ? 2 * ((size_t)T / lora_chunk(T) + 1) : 0;
 }
 
+// Rows per adapter up to which the waves take columns of their own (SHORT against rows
+// shared: 10 rows of 48 adapters at rank 16, 2048 x 8192, 18 us against 30; 80 of 30,
+// 16 and 21; 128 of 8, 10 and 9; at rank 128, where a wave holds the most sums, 170
+// rows of 48 adapters 269 and 418, 256 of 8 38 and 47, 512 of 8 65 and 68 or 84 and 78).
+static int short_rows(int r) { return r > 64 ? 256 : 80; }
 static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   const int wide = std::max(p.g[0].out ? p.g[0].C : 0, p.g[1].out ? p.g[1].C : 0);
   // up to four rank tiles a block: with eight, one wave per SIMD is left, and
   // nothing covers its waits (2000 rows of rank 128: 58 us against 38)
   const int tiles = (p.r + 15) / 16, rt = tiles <= 4 ? tiles : tiles <= 6 ? 3 : 4;
-  const dim3 grid((wide + WGRAD_COLS - 1) / WGRAD_COLS, p.T / p.chunk + p.NA + 1,
-                  2 * ((tiles + rt - 1) / rt));
+  const bool few = p.T <= short_rows(p.r) * p.NA;
+  const int cols = few ? LORA_WAVES * WGRAD_COLS : WGRAD_COLS;
+  const dim3 grid((wide + cols - 1) / cols, p.T / p.chunk + p.NA + 1, 2 * ((tiles + rt - 1) / rt));
   const dim3 block(64 * LORA_WAVES);
+  auto go = [&](auto N) {
+    constexpr int RT = decltype(N)::value;
+    if (few) hipLaunchKernelGGL((lora_wgrad_kernel<RT, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((lora_wgrad_kernel<RT, false>), grid, block, 0, s, p);
+  };
   switch (rt) {
-    case 1: hipLaunchKernelGGL((lora_wgrad_kernel<1>), grid, block, 0, s, p); break;
-    case 2: hipLaunchKernelGGL((lora_wgrad_kernel<2>), grid, block, 0, s, p); break;
-    case 3: hipLaunchKernelGGL((lora_wgrad_kernel<3>), grid, block, 0, s, p); break;
-    default: hipLaunchKernelGGL((lora_wgrad_kernel<4>), grid, block, 0, s, p); break;
+    case 1: go(std::integral_constant<int, 1>()); break;
+    case 2: go(std::integral_constant<int, 2>()); break;
+    case 3: go(std::integral_constant<int, 3>()); break;
+    default: go(std::integral_constant<int, 4>()); break;
   }
   const moe_status_t st = launch_status();
   if (st != MOE_OK || p.T <= p.chunk) return st;
@@ -1035,12 +1065,13 @@ moe_status_t moe_lora_bwd(const moe_lora_bwd_args_t* a, void* stream) {
   float* u = static_cast<float*>(a->ws);
   float* part = u + (a->T > 0 ? (size_t)a->T * a->r : 0);
   const bool want_u = a->dx_out || a->dA;
+  MOE_CHECK_ARG(aligned16(a->dA) && aligned16(a->dB));
   if (a->T > 0) {
     MOE_CHECK_ARG(a->dy && (!want_u || a->B) && (!a->dx_out || a->A) && (!a->dA || a->x) &&
                   (!a->dB || a->v));
     MOE_CHECK_ARG(aligned16(a->x) && aligned16(a->dy) && aligned16(a->A) && aligned16(a->B) &&
                   aligned16(a->v) && aligned16(a->dx) && aligned16(a->dx_out) &&
-                  aligned16(a->dA) && aligned16(a->dB) && aligned16(a->ws));
+                  aligned16(a->ws));
     if (!a->ws || a->ws_bytes < moe_lora_workspace_size(a->T, a->K, a->N, a->r, a->NA))
       return MOE_ERR_WORKSPACE;
     const size_t ny = (size_t)a->T * a->N * 2, nt = (size_t)a->T * 4, nw = (size_t)a->NA * a->r * 2;

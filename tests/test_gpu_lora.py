@@ -302,3 +302,21 @@ def test_two_streams_at_once(T, N):
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("T,NA", [(1500, 20), (2600, 40)])
+@pytest.mark.parametrize("r", [8, 24, 48, 64, 72, 128])
+def test_gradients_of_few_rows_per_adapter_but_one(r, T, NA):
+    """Few rows per adapter on average, while one adapter has more than a chunk of them: the
+    kernel that gives each wave columns of its own, with and without partial sums, onto zeros
+    and onto what is there."""
+    note(f"lora skewed rows T={T} r={r}")
+    rng = np.random.default_rng([T, r])
+    ids = np.where(rng.random(T) < 0.85, 3, rng.integers(0, NA + 1, T))
+    c = Case(T, 96, 160, r, NA, ids=ids)
+    _, v = c.forward(out=torch.empty_like(c.y[1]), want_v=True)
+    c.check_backward(c.backward(v, dx=c.dx[1], dx_out=torch.empty_like(c.dx[1])), v, c.dx[1])
+    dA = torch.full(c.A[1].shape, 0.25, device="cuda")
+    dB = torch.full(c.B[1].shape, 0.25, device="cuda")
+    res = c.backward(v, dA=dA, dB=dB, accumulate=True, want_dx=False)
+    c.check_backward(res, v, None, base=0.25)
