@@ -102,6 +102,14 @@ __device__ __forceinline__ float rest_of(float v, uint32_t b) {
   return h == v ? 0.0f : v - h;
 }
 
+// v in three bf16 parts, which hold its 24 bits.
+__device__ __forceinline__ void split3(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
+  a = bf16_of(v);
+  v = rest_of(v, a);
+  b = bf16_of(v);
+  c = bf16_of(rest_of(v, b));
+}
+
 // Four values' high and low bf16 parts.
 __device__ __forceinline__ void split_quad(const f32x4& v, u32x2& hi, u32x2& lo) {
 #pragma unroll
@@ -679,34 +687,39 @@ __device__ __forceinline__ int lora_slot(int p0, int segment, int chunk) {
   return 2 * (p0 / chunk) + (p0 == segment);
 }
 
-// A block sums one chunk of a segment for 64 columns; its waves take 32 rows at a
-// time.  The rows pass through LDS (a wave's own 32 x 64 tile, whole lines in,
-// read transposed: the reduction runs over rows), u is split into three bf16
-// parts, which hold its 24 bits, so the float32 sums are of float32 accuracy
-// at three bf16 MFMAs a step: 830 TFLOP/s of the bf16 rate against 157 of
-// v_mfma_f32.  Both gradients of 8192 rows of 8 adapters, rank 16, 4096 x 4096:
-// 30 us, 4.7 TB/s, bound by memory; at rank 64 the splitting of u, which every
-// column block repeats, takes as long as the loads (128 columns a block halve it
-// but leave too few waves: 5 to 15 % slower at every size tried).
-//
-// SHORT: each wave takes 64 columns of its own and every row, for segments that would
-// leave most waves without rows.
-template <int RT, bool SHORT>
+// A block sums one chunk of a segment; its waves take 32 rows and 64 columns at a time.
+// The rows pass through LDS (a wave's own 32 x 64 tile, whole lines in, read
+// transposed: the reduction runs over rows), u is split into three bf16 parts, which
+// hold its 24 bits, so the float32 sums are of float32 accuracy at three bf16 MFMAs
+// a step: 830 TFLOP/s of the bf16 rate against 157 of v_mfma_f32.  The waves share
+// the rows of 64 columns and add their sums at the end; or (OWN) each has 64 columns
+// and all rows, and the block splits u once for all of them, through LDS: a quarter
+// of the loads of u and of the splitting, and no idle waves where a segment has few
+// rows, but a quarter of the blocks, and two barriers a step.  Both gradients of 8192
+// rows of 8 adapters, rank 16, 4096 x 4096: 30 us, 4.7 TB/s, bound by memory; rank 64,
+// 2 adapters, 8192 x 8192: 85 us, 3.4 TB/s (shared rows 110).  128 columns a wave
+// leave too few waves: 5 to 15 % slower at every size tried.
+template <int RT, bool OWN>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraWgrad p) {
   constexpr int CT = WGRAD_COLS / 16, COLS = WGRAD_COLS;
   constexpr int CPR = COLS / 8, NX = CPR / 2;      // chunks per row, loads per step
   constexpr int RPI = 64 / CPR;                    // rows per load instruction
-  __shared__ __align__(16) uint16_t xs[LORA_WAVES][32][COLS + 8];
-  __shared__ __align__(16) float red[LORA_WAVES][16][COLS + 4];
+  constexpr int US = 32 + 8;                       // row stride of u's parts, elements
+  // a wave's rows, and when they are done with, its sums
+  __shared__ __align__(16) union {
+    uint16_t x[32][COLS + 8];
+    float sum[16][COLS + 4];
+  } lds[LORA_WAVES];
+  __shared__ __align__(16) uint16_t us[OWN ? 3 : 1][OWN ? 16 * RT : 1][US];    // [part][rank][row]
   const LoraGrad& G = p.g[blockIdx.z & 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c0 = (SHORT ? blockIdx.x * LORA_WAVES + wave : blockIdx.x) * COLS;
+  const int b0 = blockIdx.x * COLS * (OWN ? LORA_WAVES : 1), c0 = b0 + (OWN ? wave * COLS : 0);
   const int r0 = (blockIdx.z >> 1) * 16 * RT;
-  if (!G.out || c0 >= G.C) return;
+  if (!G.out || b0 >= G.C) return;
   const LoraTile tl = lora_tile<true>(p.offsets, p.NA, p.T, p.chunk, blockIdx.y);
   if (tl.n < 0 || tl.a >= p.NA) return;
-  constexpr int STEP = SHORT ? 1 : LORA_WAVES;
-  const int first = SHORT ? 0 : wave;
+  constexpr int STEP = OWN ? 1 : LORA_WAVES;
+  const int first = OWN ? 0 : wave;
   const int l = lane & 15, g = lane >> 4;
   const int xrow = lane / CPR, xcol = 8 * (lane % CPR);
   const int xc = min(c0 + xcol, G.C - 8);       // (C a multiple of 32)
@@ -726,32 +739,76 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
       x[i] = *reinterpret_cast<const u32x4*>(G.x + (size_t)max(t, 0) * G.C + xc);
     }
   };
+  // OWN: u's four rows 4 (i / 16 RT) of rank i % 16 RT, all threads of the block
+  constexpr int NU = (128 * RT + 64 * LORA_WAVES - 1) / (64 * LORA_WAVES);
+  float ua[OWN ? NU : 1][4];
+  auto fetch_u = [&](int s) {
+    if constexpr (OWN) {
+      const float* u = G.u + (size_t)(tl.p0 + 32 * s) * p.r;
+      const int last = tl.n - 1 - 32 * s;
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+        const int i = threadIdx.x + 64 * LORA_WAVES * k, row = 4 * (i / (16 * RT));
+        const int rank = min(r0 + i % (16 * RT), p.r - 1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ua[k][e] = u[(size_t)min(row + e, last) * p.r + rank];
+      }
+    }
+  };
   f32x4 acc[RT][CT] = {};
   const int steps = (tl.n + 31) / 32;
   u32x4 x[NX];
   int tok = -1, next = -1;
   if (first < steps) {          // (an adapter without rows reads nothing)
     tok = tokens(first);
+    fetch_u(first);
     fetch(tok, x);
     next = tokens(first + STEP);
   }
   for (int s = first; s < steps; s += STEP) {
     const uint32_t valid = (uint32_t)__ballot(tok >= 0);
+    if constexpr (OWN) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+        const int i = threadIdx.x + 64 * LORA_WAVES * k, row = 4 * (i / (16 * RT)), rank = i % (16 * RT);
+        if (i >= 128 * RT) break;
+        u32x2 part[3];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t b[3][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool in = r0 + rank < p.r && (valid >> (row + 2 * q + e) & 1);
+            split3(in ? ua[k][2 * q + e] : 0.0f, b[0][e], b[1][e], b[2][e]);
+          }
+#pragma unroll
+          for (int h = 0; h < 3; ++h) part[h][q] = b[h][0] | b[h][1] << 16;
+        }
+#pragma unroll
+        for (int h = 0; h < 3; ++h) *reinterpret_cast<u32x2*>(&us[h][rank][row]) = part[h];
+      }
+    }
     wave_fence();
 #pragma unroll
     for (int i = 0; i < NX; ++i)
-      *reinterpret_cast<u32x4*>(&xs[wave][RPI * i + xrow][xcol]) =
+      *reinterpret_cast<u32x4*>(&lds[wave].x[RPI * i + xrow][xcol]) =
           valid >> (RPI * i + xrow) & 1 ? x[i] : zero;
-    wave_fence();
+    if constexpr (OWN) __syncthreads();
+    else wave_fence();
     // (u's loads in front of the next rows': loads return in order)
-    const float* u = G.u + (size_t)(tl.p0 + 32 * s) * p.r;
-    const int last = tl.n - 1 - 32 * s;
-    float uv[RT][8];
+    float uv[OWN ? 1 : RT][8];
+    if constexpr (!OWN) {
+      const float* u = G.u + (size_t)(tl.p0 + 32 * s) * p.r;
+      const int last = tl.n - 1 - 32 * s;
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(r0 + 16 * j + l, p.r - 1)];
+        for (int i = 0; i < 8; ++i)
+          uv[j][i] = u[(size_t)min(8 * g + i, last) * p.r + min(r0 + 16 * j + l, p.r - 1)];
+    } else if (s + STEP < steps) {
+      fetch_u(s + STEP);
+    }
     tok = next;
     fetch(tok, x);
     next = tokens(s + 2 * STEP);
@@ -760,40 +817,42 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
     for (int i = 0; i < CT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const u32x2 v = read_tr(&xs[wave][8 * g + 4 * h + (l >> 2)][16 * i + 4 * (l & 3)]);
+        const u32x2 v = read_tr(&lds[wave].x[8 * g + 4 * h + (l >> 2)][16 * i + 4 * (l & 3)]);
         xa[i][2 * h] = v[0];
         xa[i][2 * h + 1] = v[1];
       }
     // rows without a token, and ranks past r, count as zero
-    if (valid != 0xffffffffu || r0 + 16 * RT > p.r) {
+    if constexpr (!OWN) {
+      if (valid != 0xffffffffu || r0 + 16 * RT > p.r) {
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
+        for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (r0 + 16 * j + l >= p.r || !(valid >> (8 * g + i) & 1)) uv[j][i] = 0.0f;
+          for (int i = 0; i < 8; ++i)
+            if (r0 + 16 * j + l >= p.r || !(valid >> (8 * g + i) & 1)) uv[j][i] = 0.0f;
+      }
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       u32x4 part[3];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        if constexpr (OWN) break;
         uint32_t b[3][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = uv[j][2 * q + e];
+        for (int e = 0; e < 2; ++e)
+          split3(uv[OWN ? 0 : j][2 * q + e], b[0][e], b[1][e], b[2][e]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            b[k][e] = bf16_of(v);
-            v = rest_of(v, b[k][e]);
-          }
-        }
+        for (int h = 0; h < 3; ++h) part[h][q] = b[h][0] | b[h][1] << 16;
+      }
+      if constexpr (OWN) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) part[k][q] = b[k][0] | b[k][1] << 16;
+        for (int h = 0; h < 3; ++h)
+          part[h] = *reinterpret_cast<const u32x4*>(&us[h][16 * j + l][8 * g]);
       }
 #pragma unroll
       for (int i = 0; i < CT; ++i)
 #pragma unroll
-        for (int k = 0; k < 3; ++k) acc[j][i] = mfma16(part[k], xa[i], acc[j][i]);
+        for (int h = 0; h < 3; ++h) acc[j][i] = mfma16(part[h], xa[i], acc[j][i]);
     }
   }
   // the waves in order, 16 ranks at a time
@@ -803,26 +862,26 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_wgrad_kernel(const LoraW
                      : G.part + (size_t)lora_slot(tl.p0, tl.s0, p.chunk) * p.r * G.C;
   const bool add = whole && p.accumulate;
   auto sync = [&]() {
-    if constexpr (SHORT) wave_fence();
+    if constexpr (OWN) wave_fence();
     else __syncthreads();
   };
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    if (j) sync();
+    sync();
 #pragma unroll
     for (int i = 0; i < CT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) red[wave][4 * g + q][16 * i + l] = acc[j][i][q];
+      for (int q = 0; q < 4; ++q) lds[wave].sum[4 * g + q][16 * i + l] = acc[j][i][q];
     sync();
     // four sums a lane, along the columns or (trans) the ranks
-    for (int i = SHORT ? lane : threadIdx.x; i < 4 * COLS; i += SHORT ? 64 : 64 * LORA_WAVES) {
+    for (int i = OWN ? lane : threadIdx.x; i < 4 * COLS; i += OWN ? 64 : 64 * LORA_WAVES) {
       const int rr = G.trans ? i % 4 * 4 : i / (COLS / 4), cc = G.trans ? i / 4 : i % (COLS / 4) * 4;
       const int rank = r0 + 16 * j + rr, c = c0 + cc;
       if (rank >= p.r || c >= G.C) continue;
       f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < STEP; ++k) {
-        const float(*from)[COLS + 4] = red[SHORT ? wave : k];
+        const float(*from)[COLS + 4] = lds[OWN ? wave : k].sum;
         if (G.trans) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += from[rr + e][cc];
@@ -964,23 +1023,35 @@ static size_t lora_slots(int T) {
   return T > lora_chunk(T) ? 2 * ((size_t)T / lora_chunk(T) + 1) : 0;
 }
 
-// Rows per adapter up to which the waves take columns of their own (SHORT against rows
-// shared: 10 rows of 48 adapters at rank 16, 2048 x 8192, 18 us against 30; 80 of 30,
-// 16 and 21; 128 of 8, 10 and 9; at rank 128, where a wave holds the most sums, 170
-// rows of 48 adapters 269 and 418, 256 of 8 38 and 47, 512 of 8 65 and 68 or 84 and 78).
-static int short_rows(int r) { return r > 64 ? 256 : 80; }
+// Whether the waves take columns of their own (OWN; below, against rows shared).  For
+// segments of few rows: 10 rows of 48 adapters at rank 16, 2048 x 8192, 17 us and 30;
+// 16 rows of 16 at rank 64, 4096 x 4096, 12 and 30; 88 of 8, 10 and 9.  And with as many
+// blocks as the card takes, fewer at high ranks, where u's share of the work is larger:
+// 8192 x 8192, 8192 rows of 2 at rank 64 (512 blocks) 85 and 110; of 48 at rank 128 255
+// and 426; 4096 x 4096, 8192 rows of 24 at rank 32 (768) 40 and 47, of 16 at rank 16
+// (512) 43 and 32, of 8 at rank 16 (256) 47 and 30.
+static bool own_columns(const LoraWgrad& p, int parts) {
+  const int wide = LORA_WAVES * WGRAD_COLS;
+  size_t blocks = 0;
+  for (const LoraGrad& g : p.g)
+    if (g.out) blocks += (g.C + wide - 1) / wide;
+  blocks *= (size_t)std::max(p.NA, (p.T + p.chunk - 1) / p.chunk) * parts;
+  return p.T <= 80 * p.NA || blocks >= (p.r > 48 ? 512u : 768u);
+}
+
 static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
   const int wide = std::max(p.g[0].out ? p.g[0].C : 0, p.g[1].out ? p.g[1].C : 0);
   // up to four rank tiles a block: with eight, one wave per SIMD is left, and
   // nothing covers its waits (2000 rows of rank 128: 58 us against 38)
   const int tiles = (p.r + 15) / 16, rt = tiles <= 4 ? tiles : tiles <= 6 ? 3 : 4;
-  const bool few = p.T <= short_rows(p.r) * p.NA;
-  const int cols = few ? LORA_WAVES * WGRAD_COLS : WGRAD_COLS;
-  const dim3 grid((wide + cols - 1) / cols, p.T / p.chunk + p.NA + 1, 2 * ((tiles + rt - 1) / rt));
+  const int parts = (tiles + rt - 1) / rt;
+  const bool own = own_columns(p, parts);
+  const int cols = own ? LORA_WAVES * WGRAD_COLS : WGRAD_COLS;
+  const dim3 grid((wide + cols - 1) / cols, p.T / p.chunk + p.NA + 1, 2 * parts);
   const dim3 block(64 * LORA_WAVES);
   auto go = [&](auto N) {
     constexpr int RT = decltype(N)::value;
-    if (few) hipLaunchKernelGGL((lora_wgrad_kernel<RT, true>), grid, block, 0, s, p);
+    if (own) hipLaunchKernelGGL((lora_wgrad_kernel<RT, true>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((lora_wgrad_kernel<RT, false>), grid, block, 0, s, p);
   };
   switch (rt) {
