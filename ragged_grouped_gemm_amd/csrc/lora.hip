@@ -356,12 +356,12 @@ __device__ __forceinline__ void stage_ranks(const LoraExpand& p, const LoraTile&
 // register q), so a lane ends up with two runs of 8 columns of its row and each
 // load of y and store of out covers 64 contiguous bytes of 16 rows.  A factor
 // stored the other way (TRANS) passes through LDS and is read transposed.
-template <int MT, int RT, bool TRANS>
+template <int MT, int KH, bool TRANS>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const LoraExpand p) {
-  constexpr int TM = 16 * MT, R = 16 * RT;
-  constexpr int KP = 2 * R;                 // hi and lo parts (r of each, then zeros)
+  constexpr int TM = 16 * MT, R = 32 * KH;
+  constexpr int VS = 2 * R + 8;             // a row's two parts of R ranks
   constexpr int WS = 64 + 8;                // row stride of a wave's factor tile
-  __shared__ __align__(16) uint16_t vs[TM][KP + 8];
+  __shared__ __align__(16) uint16_t vs[TM][VS];
   __shared__ __align__(16) uint16_t wt[TRANS ? LORA_WAVES : 1][TRANS ? R : 1][WS];
   const int cb = blockIdx.x % p.col_blocks;
   const LoraTile tl = lora_tile<false>(p.offsets, p.NA, p.T, TM, blockIdx.x / p.col_blocks);
@@ -401,61 +401,65 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_expand_kernel(const Lora
                        : zero;
   };
   fetch(ch);
-  stage_ranks(p, tl, TM, cb == 0, p.r, KP, &vs[0][0], KP + 8);
+  stage_ranks(p, tl, TM, cb == 0, R, 2 * R, &vs[0][0], VS);
   __syncthreads();
   if (!p.out) return;
   const uint16_t* w = p.w + (size_t)tl.a * p.r * p.C;
-  const int ksteps = (2 * p.r + 31) / 32;
   for (; ch < chunks; ch += step) {
     u32x4 yc[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 2; ++q) yc[m][q] = yr[m][q];
-    // Loads return in order, so the next chunk's y is asked for behind the
-    // factor's loads of this one: waiting for those does not wait for it.
+    // The chunk's factor in one round of loads (past r: any of its values, the rank
+    // values are zero there).  Loads return in order, so the next chunk's y is asked
+    // for behind them: waiting for the factor does not wait for it.
+    u32x4 wa[KH][4];
     if constexpr (TRANS) {
-      // eight rows of 128 bytes per instruction
-      u32x4 raw[2 * RT];
+      // eight rows of 128 bytes per instruction, turned in LDS
+      u32x4 raw[4 * KH];
       const int c = min(64 * ch + 8 * (lane & 7), p.C - 8);
 #pragma unroll
-      for (int i = 0; i < 2 * RT; ++i)
+      for (int i = 0; i < 4 * KH; ++i)
         raw[i] = *reinterpret_cast<const u32x4*>(
             w + (size_t)min(8 * i + (lane >> 3), p.r - 1) * p.C + c);
       if (ch + step < chunks) fetch(ch + step);
       wave_fence();
 #pragma unroll
-      for (int i = 0; i < 2 * RT; ++i)
+      for (int i = 0; i < 4 * KH; ++i)
         *reinterpret_cast<u32x4*>(&wt[wave][8 * i + (lane >> 3)][8 * (lane & 7)]) = raw[i];
       wave_fence();
-    }
-    f32x4 acc[MT][4] = {};
-    for (int s = 0; s < ksteps; ++s) {
-      int j = 32 * s + 8 * g;
-      j = j < p.r ? j : j < 2 * p.r ? j - p.r : 0;       // past both halves v is zero
-      u32x4 wa[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (TRANS) {
+      for (int s = 0; s < KH; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const u32x2 v = read_tr(&wt[wave][j + 4 * h + (l >> 2)][lora_column(i, l & 3)]);
-            wa[i][2 * h] = v[0];
-            wa[i][2 * h + 1] = v[1];
+            const u32x2 v =
+                read_tr(&wt[wave][32 * s + 8 * g + 4 * h + (l >> 2)][lora_column(i, l & 3)]);
+            wa[s][i][2 * h] = v[0];
+            wa[s][i][2 * h + 1] = v[1];
           }
-        } else {
+    } else {
+#pragma unroll
+      for (int s = 0; s < KH; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const int c = min(64 * ch + lora_column(i, l >> 2) + (l & 3), p.C - 1);
-          wa[i] = *reinterpret_cast<const u32x4*>(w + (size_t)c * p.r + j);
+          wa[s][i] = *reinterpret_cast<const u32x4*>(w + (size_t)c * p.r +
+                                                     min(32 * s + 8 * g, p.r - 8));
         }
-      }
-      if (!TRANS && s == ksteps - 1 && ch + step < chunks) fetch(ch + step);
+      if (ch + step < chunks) fetch(ch + step);
+    }
+    f32x4 acc[MT][4] = {};
+#pragma unroll
+    for (int s = 0; s < 2 * KH; ++s)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const u32x4 va = *reinterpret_cast<const u32x4*>(&vs[16 * m + l][32 * s + 8 * g]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = mfma16(wa[i], va, acc[m][i]);
+        for (int i = 0; i < 4; ++i) acc[m][i] = mfma16(wa[s % KH][i], va, acc[m][i]);
       }
-    }
     const int c = 64 * ch + 8 * g;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -979,11 +983,18 @@ static moe_status_t launch_expand(LoraExpand p, hipStream_t s) {
   const size_t blocks = (size_t)tiles * p.col_blocks;
   if (blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(64 * LORA_WAVES);
-  return lora_ranks(p.r, [&](auto N) {
-    constexpr int RT = decltype(N)::value;
-    if (mt == 2) hipLaunchKernelGGL((lora_expand_kernel<2, RT, TRANS>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((lora_expand_kernel<1, RT, TRANS>), grid, block, 0, s, p);
-  });
+  auto go = [&](auto N) {
+    constexpr int KH = decltype(N)::value;
+    if (mt == 2) hipLaunchKernelGGL((lora_expand_kernel<2, KH, TRANS>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((lora_expand_kernel<1, KH, TRANS>), grid, block, 0, s, p);
+  };
+  switch ((p.r + 31) / 32) {
+    case 1: go(std::integral_constant<int, 1>()); break;
+    case 2: go(std::integral_constant<int, 2>()); break;
+    case 3: go(std::integral_constant<int, 3>()); break;
+    default: go(std::integral_constant<int, 4>()); break;
+  }
+  return launch_status();
 }
 
 template <bool TRANS>
