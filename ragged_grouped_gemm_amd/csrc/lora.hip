@@ -1018,12 +1018,13 @@ static moe_status_t launch_apply(LoraExpand p, hipStream_t s) {
   return launch_status();
 }
 
-// The second half of a pass over activations: expand for few rows; apply from 64
-// rows per adapter on, if there are 2 MiB of output (1027 x 5760 at rank 64:
-// 27 us a pass with expand, 22 with apply; 512 x 4096: 11.3 and 10.9).
+// The second half of a pass over activations: expand for few rows; apply from 32
+// rows per adapter on, if there are 8 MiB of output (whole forwards, expand and apply:
+// 1027 x 5760 at rank 64 24.4 and 22.7 us, 1024 x 8192 of 32 adapters at rank 16 19.1
+// and 17.1; 512 x 4096 of 2 at rank 32 11.4 and 11.8, 4096 x 256 8.8 and 9.9).
 template <bool TRANS>
 static moe_status_t launch_out(const LoraExpand& e, hipStream_t s) {
-  const bool many = (size_t)e.T * e.C >= (1u << 20) && e.T >= 64 * e.NA;
+  const bool many = (size_t)e.T * e.C >= (1u << 22) && e.T >= 32 * e.NA;
   return e.out && many ? launch_apply<TRANS>(e, s) : launch_expand<TRANS>(e, s);
 }
 

@@ -108,10 +108,12 @@ CASES = [(1, 64, 32, 8, 1), (1, 7168, 7168, 16, 32), (7, 96, 160, 24, 3), (64, 2
          (4200, 288, 256, 16, 3), (4200, 256, 288, 40, 2), (4100, 352, 320, 88, 1),
          (4300, 288, 288, 120, 3)]
 # row tiles of 64 in the reduction, at every rank tile count (few columns: the oracle is dense)
+MANY = [(17000, 288, 256, 16, 3), (17000, 256, 288, 40, 2), (13300, 352, 320, 88, 1),
+        (14700, 288, 288, 120, 3)]      # the kernel for many rows, from 2^22 outputs on
 TALL = [(12400, 64, 96, r, 2) for r in (8, 32, 48, 64)] + [(6300, 96, 64, r, 3) for r in (72, 104)]
 
 
-@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL)
+@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL + MANY)
 def test_forward(T, K, N, r, NA):
     note(f"lora_fwd T={T} K={K} N={N} r={r} NA={NA}")
     c = Case(T, K, N, r, NA)
@@ -124,7 +126,7 @@ def test_forward(T, K, N, r, NA):
     assert none is None and inplace is c.y[1] and torch.equal(inplace, out)
 
 
-@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL)
+@pytest.mark.parametrize("T,K,N,r,NA", CASES + TALL + MANY)
 def test_backward(T, K, N, r, NA):
     note(f"lora_bwd T={T} K={K} N={N} r={r} NA={NA}")
     c = Case(T, K, N, r, NA)
@@ -277,11 +279,11 @@ def test_empty_batch_gives_zero_weight_gradients():
     ops.moe_lora_bwd(x, y, A, B, off, v, want_dw=False)
 
 
-@pytest.mark.parametrize("T,N", [(40, 256), (1500, 1024)])
+@pytest.mark.parametrize("T,N", [(40, 256), (1500, 1024), (1500, 2816)])
 def test_two_streams_at_once(T, N):
     """Calls in flight on two streams that share the adapters and the plan, each with its own
-    workspace, give the bits of calls made alone (T = 40 and 1500: the kernels for few and for
-    many rows)."""
+    workspace, give the bits of calls made alone (T = 40 and N = 2816: the kernels for few and
+    for many rows)."""
     note(f"lora two streams T={T}")
     c = [Case(T, 256, N, 16, 3, seed=s) for s in (1, 2)]
     for n in ("A", "B", "sc", "off", "src"):
