@@ -21,8 +21,8 @@
 //
 // Measured, as whole calls: 64 rows of 32 adapters, rank 16, 7168 x 7168: 11 us
 // (two launches, each at the 5 us that its chain of dependent loads takes);
-// 8192 rows of 16 adapters, rank 32, 7168 x 4096: 57 us, 4.4 TB/s of what must
-// be moved; backward of 8192 rows of 8 adapters, rank 16, 4096 x 4096: 78 us,
+// 8192 rows of 16 adapters, rank 32, 7168 x 4096: 56 us, 4.5 TB/s of what must
+// be moved; backward of 8192 rows of 8 adapters, rank 16, 4096 x 4096: 77 us,
 // 3.4 TB/s.  A large copy on the same card reaches 4.9 TB/s.
 #include "common.hpp"
 #include "spans.hpp"
