@@ -211,8 +211,11 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_shrink_kernel(const Lora
   // Every load is issued (past C: the last columns again), so that the compiler can
   // count the ones in flight; what lies past C becomes zero on its way to LDS.
   const u32x4 zero = {0, 0, 0, 0};
-  u32x4 xa[NX], wa[NW];
-  auto fetch = [&](int s) {
+  // chunks in flight: at high ranks, where few waves fit, two (4096 x 7168 of rank 128
+  // into 2048 columns, a forward: 55 us, one 62; at lower ranks no difference)
+  constexpr int DEPTH = RT >= 6 ? 2 : 1;
+  u32x4 xbuf[DEPTH][NX], wbuf[DEPTH][NW];
+  auto fetch = [&](u32x4 (&xa)[NX], u32x4 (&wa)[NW], int s) {
     const int col = min(KC * s, p.C - 8 - lc);
 #pragma unroll
     for (int i = 0; i < NX; ++i) xa[i] = *reinterpret_cast<const u32x4*>(xr[i] + col);
@@ -228,8 +231,9 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_shrink_kernel(const Lora
   // the waves of all splits of a tile (neighbours in the grid) take the chunks in
   // turn, so that together they walk the rows' lines in order
   const int stride = p.splits * LORA_WAVES, s0 = split * LORA_WAVES + wave;
-  fetch(min(s0, p.chunks - 1));
-  for (int s = s0; s < p.chunks; s += stride) {
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) fetch(xbuf[d], wbuf[d], min(s0 + d * stride, p.chunks - 1));
+  auto step = [&](u32x4 (&xa)[NX], u32x4 (&wa)[NW], int s) {
     wave_fence();
 #pragma unroll
     for (int i = 0; i < NX; ++i)
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_shrink_kernel(const Lora
         *reinterpret_cast<u32x4*>(&wt[wave][0][0] + wd[i]) = in ? wa[i] : zero;
     }
     wave_fence();
-    fetch(min(s + stride, p.chunks - 1));
+    fetch(xa, wa, min(s + DEPTH * stride, p.chunks - 1));
 #pragma unroll
     for (int k = 0; k < KC; k += 32) {
       u32x4 xf[MT], wf[RT];
@@ -267,7 +271,13 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_shrink_kernel(const Lora
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[m][j] = mfma16(wf[j], xf[m], acc[m][j]);
     }
-  }
+  };
+  for (int s = s0; s < p.chunks; s += DEPTH * stride)
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if (s + d * stride >= p.chunks) break;
+      step(xbuf[d], wbuf[d], s + d * stride);
+    }
   // the waves' sums, in wave order, 16 rows and ranks at a time
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -1041,14 +1051,15 @@ static size_t lora_slots(int T) {
 // blocks as the card takes, fewer at high ranks, where u's share of the work is larger:
 // 8192 x 8192, 8192 rows of 2 at rank 64 (512 blocks) 85 and 110; of 48 at rank 128 255
 // and 426; 4096 x 4096, 8192 rows of 24 at rank 32 (768) 40 and 47, of 16 at rank 16
-// (512) 43 and 32, of 8 at rank 16 (256) 47 and 30.
+// (512) 43 and 32, of 8 at rank 16 (256) 47 and 30; whole backwards, 6000 rows of 18 at
+// rank 40, 4096 x 5120 (648), 101 and 112.
 static bool own_columns(const LoraWgrad& p, int parts) {
   const int wide = LORA_WAVES * WGRAD_COLS;
   size_t blocks = 0;
   for (const LoraGrad& g : p.g)
     if (g.out) blocks += (g.C + wide - 1) / wide;
   blocks *= (size_t)std::max(p.NA, (p.T + p.chunk - 1) / p.chunk) * parts;
-  return p.T <= 80 * p.NA || blocks >= (p.r > 48 ? 512u : 768u);
+  return p.T <= 80 * p.NA || blocks >= (p.r > 48 ? 512u : p.r > 16 ? 640u : 768u);
 }
 
 static moe_status_t launch_wgrad(const LoraWgrad& p, hipStream_t s) {
